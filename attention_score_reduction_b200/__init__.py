@@ -3,13 +3,14 @@ per-head KV compaction on NVIDIA B200 (sm_100a).
 
 Submodules (imported on first use):
   kvzip     ctypes binding of libkvzip (the CUDA path; no CPU fallback)
+  cache     paged K/V cache (bf16, fp8, int4): write, read back, attention over it
   pipeline  end-to-end scoring -> selection -> compaction over a whole context
   synth     seeded synthetic workloads (inputs only; no method arithmetic)
   build     nvcc build of libkvzip.so
 """
 import importlib
 
-__all__ = ["kvzip", "pipeline", "synth", "build"]
+__all__ = ["kvzip", "cache", "pipeline", "synth", "build"]
 
 
 def __getattr__(name):

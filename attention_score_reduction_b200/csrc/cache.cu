@@ -1,0 +1,397 @@
+// Writing rows into the paged cache, quantised on the way, and reading them back.
+//
+// Both directions touch every byte once, so they are bound by HBM (large calls)
+// or by the launch (a decoding step's few rows).  A row of d elements is the
+// work of d / 8 lanes, 16 bytes of bf16 each, so that a half warp (d = 128) or a
+// warp (d = 256) moves whole 128-byte lines and a row's extremes cost four or
+// five shuffles.  A warp takes `chunk` consecutive rows: lane i finds where row i
+// goes (unit, page, pool row) for all of them at once, which keeps the dependent
+// loads (offsets, start, page table) off the rows' own path, and the lanes of a
+// row get its address by a shuffle.
+//
+// Quantisation (one row x of one unit):
+//   fp8   e = smallest integer >= -126 with max|x| <= 448 * 2^e (0 for a zero
+//         row); code = e4m3(x * 2^-e).  The scale is a power of two, so x * 2^-e
+//         is exact, the one rounding is the e4m3 conversion's, and the value
+//         code * 2^e is exact in bf16.  A non-finite element makes the scale NaN:
+//         the whole row reads back as NaN.
+//   int4  z = min x (exact in bf16), s = bf16((max - min) / 15), code = the
+//         integer nearest (x - z) / s (ties to even, 0 where s = 0), held to 15.
+//         A non-finite element, or one of magnitude 2^126 or more (its range
+//         would overflow), makes s and z NaN.
+// The scale s = bf16((max - min) / 15) is the same from 32 bits as from exact
+// arithmetic: a quotient within 2^-23 of a midpoint between two bf16 numbers m
+// needs max - min = 15 m (1 + tiny), but 15 m has 12 or 13 significant bits and
+// max and min have 8 each, so they are equal or at least 2^-20 apart.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "cache.cuh"
+#include "kvzip_internal.h"
+
+namespace kvzip {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr float kInt4Limit = 8.507059173023462e37f;   // 2^126
+
+// Unit and row of flat row r: dense r = u * n_rows + t; packed offsets[u] <= r <
+// offsets[u + 1].  Returns false where no unit owns the row.
+__device__ __forceinline__ bool row_owner(const int64_t* offsets, int64_t units, int64_t n_rows,
+                                          int64_t r, int64_t* u, int64_t* t) {
+  if (offsets == nullptr) {
+    *u = r / n_rows;
+    *t = r - *u * n_rows;
+    return *u < units;
+  }
+  int64_t lo = 0, hi = units;            // offsets[lo] <= r (or lo = 0), r < offsets[hi] (or hi = units)
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (offsets[mid] <= r) lo = mid; else hi = mid;
+  }
+  *u = lo;
+  *t = r - offsets[lo];
+  return *t >= 0 && r < offsets[lo + 1];
+}
+
+// Rows the call brings for unit u.
+__device__ __forceinline__ int64_t rows_of(const CacheWriteArgs& a, int64_t u) {
+  if (a.offsets != nullptr) {
+    const int64_t lo = a.offsets[u], hi = a.offsets[u + 1];
+    if (lo < 0 || hi < lo || hi > a.n_rows) atomicOr(a.c.status, kStatusBadCache);
+    const int64_t n = (hi > a.n_rows ? a.n_rows : hi) - (lo < 0 ? 0 : lo);
+    return n < 0 ? 0 : n;
+  }
+  return a.counts == nullptr ? a.n_rows
+                             : held_to(a.counts[u], static_cast<int>(a.n_rows), a.c.status);
+}
+
+__device__ __forceinline__ void advance_len(const CacheWriteArgs& a, int64_t u, int first) {
+  const int cap = cache_cap(a.c);
+  a.c.lens[u] = held_to(first + rows_of(a, u), cap, a.c.status);
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int w = LPR / 2; w >= 1; w >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, w));
+  return v;
+}
+
+// Stores this lane's eight elements (four bf16 pairs) of a row.
+template <int FMT, int D>
+__device__ __forceinline__ void store_row(uint8_t* pages, uint32_t* params, int64_t slot, int lr,
+                                          const uint4 raw, bool live) {
+  constexpr int LPR = D / 8;
+  if constexpr (FMT == kFmtBf16) {
+    if (live)
+      *reinterpret_cast<uint4*>(pages + slot * CacheRow<FMT, D>::BYTES + lr * 16) = raw;
+    return;
+  }
+  float x[8];
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+  if constexpr (FMT == kFmtFp8) {
+    // the largest magnitude by the order of the bits, where a NaN ranks above
+    // infinity and so is seen
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      top = max(top, (w[i] << 16) & 0x7fff0000u);
+      top = max(top, w[i] & 0x7fff0000u);
+    }
+#pragma unroll
+    for (int k = LPR / 2; k >= 1; k >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
+    // 448 * 2^e = 1.75 * 2^(e + 8): e from the exponent, one more above 1.75
+    int e = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
+    e = top == 0 ? 0 : max(e, -126);
+    const bool bad = top >= 0x7f800000u;
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);   // 2^-e
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = pack_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+    if (live) {
+      // a bad row's codes are zeros: NaN lives in parameters only, which the
+      // attention applies after its mask
+      *reinterpret_cast<uint2*>(pages + slot * CacheRow<FMT, D>::BYTES + lr * 8) =
+          bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+      if (lr == 0)
+        params[slot] = bad ? 0x7fc00000u : static_cast<uint32_t>(127 + e) << 23;
+    }
+  } else {
+    float lo = x[0], hi = x[0];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      lo = fminf(lo, x[i]);
+      hi = fmaxf(hi, x[i]);
+      bad |= !(fabsf(x[i]) < kInt4Limit);
+    }
+    lo = -row_max<LPR>(-lo);
+    hi = row_max<LPR>(hi);
+    const uint32_t votes = __ballot_sync(0xffffffffu, bad);
+    bad = LPR == 32 ? votes != 0
+                    : ((votes >> (threadIdx.x & 16)) & 0xffffu) != 0;
+    const uint32_t par = bad ? 0x7fc07fc0u : pack_bf16x2((hi - lo) / 15.f, lo);
+    float s = bf16_lo(par);
+    // tiny scales are lifted by 2^100 (exactly), so that 1 / s stays finite
+    const float lift = s < 8.6736174e-19f ? 1.2676506e30f : 1.f;
+    const float zl = -lo * lift;
+    s *= lift;
+    const float inv = s > 0.f ? 1.f / s : 0.f;
+    const float half = s > 0.f ? 0.5f * s : INFINITY;
+    uint32_t code[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float d = fmaf(x[i], lift, zl);      // x - z, rounded once
+      int c = __float2int_rn(d * inv);
+      const float r = fmaf(static_cast<float>(-c), s, d);   // exact: |r| is at most about s / 2
+      if (fabsf(r) >= 0.4999f * s) {
+        // next to a border between two codes: settle it with the error of d
+        const float a = x[i] * lift, bb = d - a;
+        const float err = (a - (d - bb)) + (zl - bb);
+        if (r > half || (r == half && (err > 0.f || (err == 0.f && (c & 1))))) ++c;
+        if (r < -half || (r == -half && (err < 0.f || (err == 0.f && (c & 1))))) --c;
+      }
+      code[i] = static_cast<uint32_t>(min(max(c, 0), 15));
+    }
+    if (live) {
+      uint32_t word = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) word |= code[i] << (4 * i);
+      *reinterpret_cast<uint32_t*>(pages + slot * CacheRow<FMT, D>::BYTES + lr * 4) = word;
+      if (lr == 0) params[slot] = par;
+    }
+  }
+}
+
+// This lane's eight elements of a stored row as four bf16 pairs.
+template <int FMT, int D>
+__device__ __forceinline__ uint4 load_row(const uint8_t* pages, const uint32_t* params, int64_t slot,
+                                          int lr, bool live) {
+  if (!live) return make_uint4(0, 0, 0, 0);
+  const uint8_t* p = pages + slot * CacheRow<FMT, D>::BYTES;
+  if constexpr (FMT == kFmtBf16) {
+    return ldg_stream16(p + lr * 16);
+  } else if constexpr (FMT == kFmtFp8) {
+    const uint2 c = ldg_stream8(p + lr * 8);
+    const float s = __uint_as_float(params[slot]);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = e4m3x2_f16x2(i < 2 ? c.x >> (16 * i) : c.y >> (16 * (i - 2)));
+      float f0, f1;
+      asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\t"
+          "cvt.f32.f16 %1, b;\n\t}"
+          : "=f"(f0), "=f"(f1)
+          : "r"(h));
+      o[i] = pack_bf16x2(f0 * s, f1 * s);   // exact: 4 significant bits and a power of two
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  } else {
+    const uint32_t c = *reinterpret_cast<const uint32_t*>(p + lr * 4);
+    const uint32_t par = params[slot];
+    const float s = bf16_lo(par), z = bf16_hi(par);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = pack_bf16x2(fmaf(static_cast<float>((c >> (8 * i)) & 15u), s, z),
+                         fmaf(static_cast<float>((c >> (8 * i + 4)) & 15u), s, z));
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// mode 0: lens left to another launch; 1: starts and lens are different buffers,
+// any thread may write lens; 2: append, a warp's chunk is one whole unit.
+template <int FMT, int D>
+__global__ void __launch_bounds__(kRowThreads)
+    cache_write_rows(const CacheWriteArgs a, int64_t total, int chunk, int mode) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, UNR = 4;
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
+  if (mode == 1) {
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; u < a.c.units;
+         u += step)
+      advance_len(a, u, held_to(a.starts[u], cache_cap(a.c), a.c.status));
+  }
+  const int64_t r0 = warp * chunk;
+  // lane i: where row r0 + i comes from and goes to
+  int64_t slot = -1, ksrc = 0, vsrc = 0;
+  if (lane < chunk && r0 + lane < total) {
+    int64_t u, t;
+    if (row_owner(a.offsets, a.c.units, a.n_rows, r0 + lane, &u, &t) && t < rows_of(a, u)) {
+      const int cap = cache_cap(a.c);
+      const int64_t pos =
+          held_to(a.starts ? a.starts[u] : a.c.lens[u], cap, a.c.status) + t;
+      if (pos < cap)
+        slot = cache_slot(a.c, u, static_cast<int>(pos));
+      else
+        atomicOr(a.c.status, kStatusBadCache);
+      ksrc = a.offsets ? (r0 + lane) * a.k_row : u * a.k_unit + t * a.k_row;
+      vsrc = a.offsets ? (r0 + lane) * a.v_row : u * a.v_unit + t * a.v_row;
+    }
+  }
+  __syncwarp();
+  if (mode == 2 && lane == 0 && warp < a.c.units)
+    advance_len(a, warp, held_to(a.c.lens[warp], cache_cap(a.c), a.c.status));
+  if (__all_sync(0xffffffffu, slot < 0)) return;
+  const int sub = lane / LPR, lr = lane % LPR;
+  const uint16_t* kp = static_cast<const uint16_t*>(a.k) + lr * 8;
+  const uint16_t* vp = static_cast<const uint16_t*>(a.v) + lr * 8;
+  for (int i0 = 0; i0 < chunk; i0 += UNR * RPW) {
+    int64_t sl[UNR];
+    uint4 kr[UNR], vr[UNR];
+#pragma unroll
+    for (int j = 0; j < UNR; ++j) {
+      const int i = i0 + j * RPW + sub;          // i >= chunk: its lane holds slot = -1, or i >= 32
+      sl[j] = __shfl_sync(0xffffffffu, slot, i & 31);
+      const int64_t ks = __shfl_sync(0xffffffffu, ksrc, i & 31);
+      const int64_t vs = __shfl_sync(0xffffffffu, vsrc, i & 31);
+      if (i >= chunk) sl[j] = -1;
+      if (sl[j] >= 0) {
+        kr[j] = ldg_stream16(kp + ks);
+        vr[j] = ldg_stream16(vp + vs);
+      } else {
+        kr[j] = vr[j] = make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < UNR; ++j) {
+      store_row<FMT, D>(static_cast<uint8_t*>(a.c.k_pages), a.c.k_params, sl[j], lr, kr[j],
+                        sl[j] >= 0);
+      store_row<FMT, D>(static_cast<uint8_t*>(a.c.v_pages), a.c.v_params, sl[j], lr, vr[j],
+                        sl[j] >= 0);
+    }
+  }
+}
+
+// Appends of many rows: lens moves on once every row has read the old one.
+__global__ void cache_advance(const CacheWriteArgs a) {
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (u < a.c.units) advance_len(a, u, held_to(a.c.lens[u], cache_cap(a.c), a.c.status));
+}
+
+template <int FMT, int D>
+__global__ void __launch_bounds__(kRowThreads)
+    cache_read_rows(const CacheReadArgs a, int64_t total, int chunk) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR, UNR = 4;
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
+  const int64_t r0 = warp * chunk;
+  int64_t slot = -1;
+  if (lane < chunk && r0 + lane < total) {
+    int64_t u, t;
+    if (row_owner(a.offsets, a.c.units, a.n_rows, r0 + lane, &u, &t)) {
+      const int cap = cache_cap(a.c);
+      const int64_t pos = (a.starts ? held_to(a.starts[u], cap, a.c.status) : 0) + t;
+      if (pos < held_to(a.c.lens[u], cap, a.c.status))
+        slot = cache_slot(a.c, u, static_cast<int>(pos));
+    }
+  }
+  if (__all_sync(0xffffffffu, slot < 0)) return;
+  const int sub = lane / LPR, lr = lane % LPR;
+  for (int i0 = 0; i0 < chunk; i0 += UNR * RPW) {
+    int64_t sl[UNR];
+    uint4 kr[UNR], vr[UNR];
+#pragma unroll
+    for (int j = 0; j < UNR; ++j) {
+      const int i = i0 + j * RPW + sub;
+      sl[j] = __shfl_sync(0xffffffffu, slot, i & 31);
+      if (i >= chunk) sl[j] = -1;
+      kr[j] = load_row<FMT, D>(static_cast<const uint8_t*>(a.c.k_pages), a.c.k_params, sl[j], lr,
+                               sl[j] >= 0);
+      vr[j] = load_row<FMT, D>(static_cast<const uint8_t*>(a.c.v_pages), a.c.v_params, sl[j], lr,
+                               sl[j] >= 0);
+    }
+#pragma unroll
+    for (int j = 0; j < UNR; ++j) {
+      if (sl[j] < 0) continue;
+      const int64_t o = (r0 + i0 + j * RPW + sub) * D + lr * 8;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_out) + o) = kr[j];
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_out) + o) = vr[j];
+    }
+  }
+}
+
+// Rows a warp takes: 32 (one address per lane) when that still gives every SM a
+// few warps, else fewer, so that a short call spreads over the machine.
+int rows_per_warp(int64_t total) {
+  int chunk = 32;
+  while (chunk > 2 && total / chunk < 148 * 16) chunk >>= 1;
+  return chunk;
+}
+
+template <int FMT, int D>
+cudaError_t write_fd(const CacheWriteArgs& a, cudaStream_t s, int* launches) {
+  const int64_t total = a.offsets ? a.n_rows : a.c.units * a.n_rows;
+  int mode = a.starts ? 1 : 0;
+  int chunk = rows_per_warp(total);
+  int64_t warps = (total + chunk - 1) / chunk;
+  if (!a.starts && !a.offsets && a.n_rows > 0 && a.n_rows <= 32) {
+    mode = 2;
+    chunk = static_cast<int>(a.n_rows);
+    warps = a.c.units;
+  }
+  const int per_block = kRowThreads / 32;
+  int64_t blocks = (warps + per_block - 1) / per_block;
+  if (blocks < 1) blocks = 1;     // no rows: lens may still change (starts given)
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  cache_write_rows<FMT, D><<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(a, total, chunk,
+                                                                                mode);
+  *launches += 1;
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || mode != 0) return e;
+  cache_advance<<<static_cast<unsigned>((a.c.units + 127) / 128), 128, 0, s>>>(a);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+template <int FMT, int D>
+cudaError_t read_fd(const CacheReadArgs& a, cudaStream_t s, int* launches) {
+  const int64_t total = a.offsets ? a.n_rows : a.c.units * a.n_rows;
+  const int chunk = rows_per_warp(total);
+  const int64_t warps = (total + chunk - 1) / chunk;
+  const int per_block = kRowThreads / 32;
+  const int64_t blocks = (warps + per_block - 1) / per_block;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  cache_read_rows<FMT, D><<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(a, total, chunk);
+  *launches += 1;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t bounds_flag_cache(unsigned int* out) { return take_bounds_flag(out); }
+
+cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t s, int* launches) {
+  switch (a.c.format * 1000 + a.c.d) {
+    case kFmtBf16 * 1000 + 128: return write_fd<kFmtBf16, 128>(a, s, launches);
+    case kFmtBf16 * 1000 + 256: return write_fd<kFmtBf16, 256>(a, s, launches);
+    case kFmtFp8 * 1000 + 128: return write_fd<kFmtFp8, 128>(a, s, launches);
+    case kFmtFp8 * 1000 + 256: return write_fd<kFmtFp8, 256>(a, s, launches);
+    case kFmtInt4 * 1000 + 128: return write_fd<kFmtInt4, 128>(a, s, launches);
+    case kFmtInt4 * 1000 + 256: return write_fd<kFmtInt4, 256>(a, s, launches);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t s, int* launches) {
+  switch (a.c.format * 1000 + a.c.d) {
+    case kFmtBf16 * 1000 + 128: return read_fd<kFmtBf16, 128>(a, s, launches);
+    case kFmtBf16 * 1000 + 256: return read_fd<kFmtBf16, 256>(a, s, launches);
+    case kFmtFp8 * 1000 + 128: return read_fd<kFmtFp8, 128>(a, s, launches);
+    case kFmtFp8 * 1000 + 256: return read_fd<kFmtFp8, 256>(a, s, launches);
+    case kFmtInt4 * 1000 + 128: return read_fd<kFmtInt4, 128>(a, s, launches);
+    case kFmtInt4 * 1000 + 256: return read_fd<kFmtInt4, 256>(a, s, launches);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace kvzip

@@ -1,0 +1,91 @@
+// The paged key/value cache as the device code sees it, shared by the kernels
+// that write it, read it back and attend over it.
+//
+// A unit is one KV head of one sequence.  Row `pos` of unit u lies in page
+// page_table[u][pos / page_rows], at row pos % page_rows of that page.  Formats:
+//   bf16  the row itself (2 d bytes)
+//   fp8   d e4m3 codes; parameter word = float32 scale 2^e; value = code * 2^e
+//   int4  d/2 bytes, element 2b in the low nibble of byte b; parameter word =
+//         bf16 scale s (low half) and bf16 zero z (high half); value = s c + z
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kvzip_internal.h"
+
+namespace kvzip {
+
+enum : int { kFmtBf16 = 0, kFmtFp8 = 1, kFmtInt4 = 2 };
+
+template <int FMT, int D>
+struct CacheRow {
+  static constexpr int BYTES = FMT == kFmtBf16 ? 2 * D : (FMT == kFmtFp8 ? D : D / 2);
+};
+
+// Rows a unit can hold (the host keeps it below 2^31).
+__device__ __forceinline__ int cache_cap(const CacheArgs& c) { return c.max_pages << c.page_shift; }
+
+// n held to [0, hi]; anything outside sets the status bit.
+__device__ __forceinline__ int held_to(int64_t n, int hi, uint32_t* status) {
+  if (n >= 0 && n <= hi) return static_cast<int>(n);
+  atomicOr(status, kStatusBadCache);
+  return n < 0 ? 0 : hi;
+}
+
+// Pool row of position pos of unit u (0 <= pos < max_pages * page_rows), or -1
+// (and the status bit) where the page table names no page of the pool.
+__device__ __forceinline__ int64_t cache_slot(const CacheArgs& c, int64_t u, int pos) {
+  const int page = c.page_table[u * c.max_pages + (pos >> c.page_shift)];
+  if (page < 0 || page >= c.n_pages) {
+    atomicOr(c.status, kStatusBadCache);
+    return -1;
+  }
+  return (static_cast<int64_t>(page) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// two floats as bf16x2 (x in the low half), round to nearest even
+__device__ __forceinline__ uint32_t pack_bf16x2(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+// two floats as f16x2 (x in the low half), round to nearest even
+__device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+// two e4m3 codes (low byte first) as f16x2: exact
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
+  return r;
+}
+// two floats as e4m3 codes (x in the low byte), round to nearest even
+__device__ __forceinline__ uint32_t pack_e4m3x2(float x, float y) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+  return r;
+}
+
+// 16-byte read-only load that is not kept in L1 (each cache byte is used once per CTA)
+__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "l"(p));
+  return v;
+}
+
+}  // namespace kvzip

@@ -1,0 +1,42 @@
+// Shared by the attention kernels over the paged cache: storing output rows and
+// merging the partial results of items that several CTAs worked on.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "cache_sched.cuh"
+
+namespace kvzip {
+
+// Eight consecutive elements of query row `row` of an item.
+__device__ __forceinline__ void attn_store8(const CacheAttnArgs& a, const AttnShape& s,
+                                            const AttnItem& it, int row, int e,
+                                            const float (&v)[8]) {
+  const int r = it.row0 + row, tok = r / s.G, g = r - tok * s.G;
+  const int64_t at = it.u * a.o_unit + g * a.o_head + tok * a.o_row + e;
+  if (a.out_f32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                   pack_bf16x2(v[6], v[7]));
+  }
+}
+
+inline size_t attn_ml_bytes(int64_t rows) {
+  return (static_cast<size_t>(rows) * sizeof(float2) + 255) / 256 * 256;
+}
+
+// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the CTAs of each item
+// that no CTA covered whole; zeros for items (and rows) that see nothing.  Slot
+// cta + item holds shape.block rows of (m, l) and of o[d].
+cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, int64_t items,
+                              int ctas, const float2* ml, const float* o, cudaStream_t st);
+
+int rows_ctas(int format, int d);
+cudaError_t launch_cache_attn_rows(const CacheAttnArgs& a, cudaStream_t s, int* launches);
+
+}  // namespace kvzip

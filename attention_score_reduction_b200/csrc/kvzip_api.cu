@@ -60,7 +60,7 @@ kvzip_status kvzip_debug_bounds_status(void) {
   unsigned int any = 0;
   cudaError_t (*const files[])(unsigned int*) = {
       kvzip::bounds_flag_score, kvzip::bounds_flag_select, kvzip::bounds_flag_select_fused,
-      kvzip::bounds_flag_compact, kvzip::bounds_flag_decode};
+      kvzip::bounds_flag_compact, kvzip::bounds_flag_decode, kvzip::bounds_flag_cache};
   for (auto take : files) {
     unsigned int f = 0;
     if (take(&f) != cudaSuccess) return KVZIP_ERR_CUDA;
@@ -210,7 +210,8 @@ kvzip_status kvzip_workspace_status(void* workspace, void* stream) {
   if (cudaMemcpy(workspace, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
     return KVZIP_ERR_CUDA;
   if (word & kvzip::kStatusTimeout) return KVZIP_ERR_TIMEOUT;
-  return (word & kvzip::kStatusHistMismatch) ? KVZIP_ERR_INVALID_ARG : KVZIP_OK;
+  return (word & (kvzip::kStatusHistMismatch | kvzip::kStatusBadCache)) ? KVZIP_ERR_INVALID_ARG
+                                                                        : KVZIP_OK;
 }
 
 int64_t kvzip_keep_count(double r, int64_t N) {
@@ -456,6 +457,168 @@ kvzip_status kvzip_decode_attention(const void* q, const void* k_packed, const v
   a.timeout_ns = g_timeout_ns.load();
   int launches = 0;
   cudaError_t e = kvzip::launch_decode(a, static_cast<cudaStream_t>(stream), &launches);
+  if (e == cudaSuccess) g_last_launches.store(launches);
+  return from_cuda(e);
+}
+
+// Host checks of a paged cache; on success fills the kernels' view of it.
+static kvzip_status cache_args(const kvzip_cache* c, kvzip::CacheArgs* a) {
+  if (!c) return KVZIP_ERR_INVALID_ARG;
+  if (c->format != KVZIP_CACHE_BF16 && c->format != KVZIP_CACHE_FP8 &&
+      c->format != KVZIP_CACHE_INT4)
+    return KVZIP_ERR_INVALID_ARG;
+  if (c->d != 128 && c->d != 256) return c->d > 0 ? KVZIP_ERR_UNSUPPORTED : KVZIP_ERR_INVALID_ARG;
+  int shift = 4;
+  while (shift < 7 && (1 << shift) != c->page_rows) ++shift;
+  if ((1 << shift) != c->page_rows)
+    return c->page_rows > 0 ? KVZIP_ERR_UNSUPPORTED : KVZIP_ERR_INVALID_ARG;
+  if (c->units < 0 || c->n_pages <= 0 || c->max_pages <= 0) return KVZIP_ERR_INVALID_ARG;
+  if (c->units > (int64_t{1} << 24) || c->n_pages > (INT32_MAX >> shift) ||
+      c->max_pages > (INT32_MAX >> shift))
+    return KVZIP_ERR_UNSUPPORTED;
+  if (!c->k_pages || !c->v_pages || !c->page_table || !c->lens || !c->status)
+    return KVZIP_ERR_INVALID_ARG;
+  if (c->format != KVZIP_CACHE_BF16 && (!c->k_params || !c->v_params)) return KVZIP_ERR_INVALID_ARG;
+  if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->k_params, 16) ||
+      !aligned(c->v_params, 16) || !aligned(c->page_table, 4) || !aligned(c->lens, 4) ||
+      !aligned(c->status, 4))
+    return KVZIP_ERR_INVALID_ARG;
+  a->format = c->format;
+  a->d = c->d;
+  a->page_shift = shift;
+  a->max_pages = c->max_pages;
+  a->n_pages = c->n_pages;
+  a->units = c->units;
+  a->k_pages = c->k_pages;
+  a->v_pages = c->v_pages;
+  a->k_params = c->k_params;
+  a->v_params = c->v_params;
+  a->page_table = c->page_table;
+  a->lens = c->lens;
+  a->status = c->status;
+  return KVZIP_OK;
+}
+
+// Rows of a call: at most 2^31 - 1 in all, so that kernels count them in 64 bits safely.
+static bool rows_ok(int64_t units, int64_t n_rows, bool packed) {
+  if (n_rows < 0 || n_rows > INT32_MAX) return false;
+  return packed || units == 0 || n_rows <= (int64_t{1} << 36) / units;
+}
+
+static bool stride8(int64_t s) { return s >= 0 && s % 8 == 0; }
+
+kvzip_status kvzip_cache_write(const kvzip_cache* cache, const void* k, const void* v,
+                               int64_t k_unit_stride, int64_t k_row_stride,
+                               int64_t v_unit_stride, int64_t v_row_stride, int64_t n_rows,
+                               const int32_t* starts, const int32_t* counts,
+                               const int64_t* offsets, void* stream) {
+  kvzip::CacheWriteArgs a;
+  const kvzip_status st = cache_args(cache, &a.c);
+  if (st != KVZIP_OK) return st;
+  if (n_rows < 0) return KVZIP_ERR_INVALID_ARG;
+  if (!rows_ok(cache->units, n_rows, offsets != nullptr)) return KVZIP_ERR_UNSUPPORTED;
+  if (n_rows > 0 && (!k || !v)) return KVZIP_ERR_INVALID_ARG;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(counts, 4) ||
+      !aligned(offsets, 8))
+    return KVZIP_ERR_INVALID_ARG;
+  if (!stride8(k_row_stride) || !stride8(v_row_stride) || !stride8(k_unit_stride) ||
+      !stride8(v_unit_stride))
+    return KVZIP_ERR_INVALID_ARG;
+  if (counts && offsets) return KVZIP_ERR_INVALID_ARG;
+  if (cache->units == 0) return KVZIP_OK;
+  a.k = k;
+  a.v = v;
+  a.k_unit = k_unit_stride;
+  a.k_row = k_row_stride;
+  a.v_unit = v_unit_stride;
+  a.v_row = v_row_stride;
+  a.n_rows = n_rows;
+  a.starts = starts == cache->lens ? nullptr : starts;
+  a.counts = counts;
+  a.offsets = offsets;
+  int launches = 0;
+  const cudaError_t e = kvzip::launch_cache_write(a, static_cast<cudaStream_t>(stream), &launches);
+  if (e == cudaSuccess) g_last_launches.store(launches);
+  return from_cuda(e);
+}
+
+kvzip_status kvzip_cache_read(const kvzip_cache* cache, void* k_out, void* v_out, int64_t n_rows,
+                              const int32_t* starts, const int64_t* offsets, void* stream) {
+  kvzip::CacheReadArgs a;
+  const kvzip_status st = cache_args(cache, &a.c);
+  if (st != KVZIP_OK) return st;
+  if (n_rows < 0) return KVZIP_ERR_INVALID_ARG;
+  if (!rows_ok(cache->units, n_rows, offsets != nullptr)) return KVZIP_ERR_UNSUPPORTED;
+  if (cache->units == 0 || n_rows == 0) return KVZIP_OK;
+  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(starts, 4) ||
+      !aligned(offsets, 8))
+    return KVZIP_ERR_INVALID_ARG;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.n_rows = n_rows;
+  a.starts = starts;
+  a.offsets = offsets;
+  int launches = 0;
+  const cudaError_t e = kvzip::launch_cache_read(a, static_cast<cudaStream_t>(stream), &launches);
+  if (e == cudaSuccess) g_last_launches.store(launches);
+  return from_cuda(e);
+}
+
+constexpr int kMaxG = 64;
+
+size_t kvzip_cache_attention_workspace_size(const kvzip_cache* cache, int G, int n_q) {
+  kvzip::CacheArgs c;
+  if (cache_args(cache, &c) != KVZIP_OK || G <= 0 || G > kMaxG || n_q < 0) return 0;
+  if (cache->units == 0 || n_q == 0) return 0;
+  return kvzip::cache_attn_ws_bytes(c.units, G, n_q, c.d, c.format);
+}
+
+kvzip_status kvzip_cache_attention(const kvzip_cache* cache, const void* q, int64_t q_unit_stride,
+                                   int64_t q_head_stride, int64_t q_row_stride, void* out,
+                                   int out_f32, int64_t out_unit_stride, int64_t out_head_stride,
+                                   int64_t out_row_stride, const int32_t* q_lens, int n_q, int G,
+                                   float scale, void* workspace, size_t ws_bytes, void* stream) {
+  kvzip::CacheAttnArgs a;
+  const kvzip_status st = cache_args(cache, &a.c);
+  if (st != KVZIP_OK) return st;
+  if (G <= 0 || n_q < 0) return KVZIP_ERR_INVALID_ARG;
+  // items (blocks of at least 8 query rows) and their slots are counted in 31 bits
+  if (G > kMaxG || n_q > (1 << 24) ||
+      (static_cast<int64_t>(n_q) * G / 8 + 1) * cache->units > INT32_MAX / 2)
+    return KVZIP_ERR_UNSUPPORTED;
+  if (cache->units == 0 || n_q == 0) return KVZIP_OK;
+  if (!q || !out || !workspace) return KVZIP_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256) || !aligned(q_lens, 4))
+    return KVZIP_ERR_INVALID_ARG;
+  if (!stride8(q_unit_stride) || !stride8(q_head_stride) || !stride8(q_row_stride) ||
+      !stride8(out_unit_stride) || !stride8(out_head_stride) || !stride8(out_row_stride))
+    return KVZIP_ERR_INVALID_ARG;
+  if ((cache->units > 1 && out_unit_stride < cache->d) || (G > 1 && out_head_stride < cache->d) ||
+      (n_q > 1 && out_row_stride < cache->d))
+    return KVZIP_ERR_INVALID_ARG;
+  if (ws_bytes < kvzip_cache_attention_workspace_size(cache, G, n_q)) return KVZIP_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || std::isinf(scale)) scale = 1.0f / std::sqrt(static_cast<float>(cache->d));
+  a.q = q;
+  a.q_unit = q_unit_stride;
+  a.q_head = q_head_stride;
+  a.q_row = q_row_stride;
+  a.out = out;
+  a.out_f32 = out_f32 != 0;
+  a.o_unit = out_unit_stride;
+  a.o_head = out_head_stride;
+  a.o_row = out_row_stride;
+  a.q_lens = q_lens;
+  a.n_q = n_q;
+  a.G = G;
+  a.scale = scale;
+  a.ws = workspace;
+  a.ws_bytes = ws_bytes;
+  a.timeout_ns = g_timeout_ns.load();
+  a.test_stall = g_test_stall.load();
+  int launches = 0;
+  const cudaError_t e =
+      kvzip::launch_cache_attention(a, static_cast<cudaStream_t>(stream), &launches);
+  if (e == cudaErrorInvalidValue) return KVZIP_ERR_INVALID_ARG;   // tensor map rejected the pools
   if (e == cudaSuccess) g_last_launches.store(launches);
   return from_cuda(e);
 }

@@ -10,6 +10,7 @@ namespace kvzip {
 // Status bits the kernels OR into the workspace header word.
 constexpr uint32_t kStatusTimeout = 1u;
 constexpr uint32_t kStatusHistMismatch = 2u;   // kvzip_select_hist: histogram != scores
+constexpr uint32_t kStatusBadCache = 4u;       // paged cache: a length or page id out of range
 
 // Bytes reserved at the front of the scoring workspace for the status word.
 constexpr size_t kScoreWsHeader = 256;
@@ -125,6 +126,59 @@ size_t decode_ml_bytes(int64_t n_heads, int G);
 size_t decode_ws_bytes(int64_t n_heads, int G, int d);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s, int* launches);
 
+// The paged cache (kvzip_cache) as the kernels take it: page_rows = 1 << page_shift.
+struct CacheArgs {
+  int format, d, page_shift, max_pages;
+  int64_t n_pages, units;
+  void* k_pages;
+  void* v_pages;
+  uint32_t* k_params;
+  uint32_t* v_params;
+  const int32_t* page_table;
+  int32_t* lens;
+  uint32_t* status;
+};
+
+struct CacheWriteArgs {
+  CacheArgs c;
+  const void* k;
+  const void* v;
+  int64_t k_unit, k_row, v_unit, v_row;   // strides in elements
+  int64_t n_rows;                         // rows per unit (dense), or of all units (packed)
+  const int32_t* starts;                  // first position per unit, or null: lens
+  const int32_t* counts;                  // dense: rows of each unit, or null: n_rows
+  const int64_t* offsets;                 // packed: [units + 1], or null: dense
+};
+cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t s, int* launches);
+
+struct CacheReadArgs {
+  CacheArgs c;
+  void* k_out;
+  void* v_out;
+  int64_t n_rows;                         // as in CacheWriteArgs
+  const int32_t* starts;                  // first position per unit, or null: 0
+  const int64_t* offsets;
+};
+cudaError_t launch_cache_read(const CacheReadArgs& a, cudaStream_t s, int* launches);
+
+struct CacheAttnArgs {
+  CacheArgs c;
+  const void* q;
+  int64_t q_unit, q_head, q_row;          // strides in elements
+  void* out;
+  int64_t o_unit, o_head, o_row;
+  int out_f32;
+  const int32_t* q_lens;                  // new tokens per unit, or null: n_q
+  int n_q, G;
+  float scale;
+  void* ws;
+  size_t ws_bytes;
+  uint64_t timeout_ns;
+  int test_stall;
+};
+size_t cache_attn_ws_bytes(int64_t units, int G, int n_q, int d, int format);
+cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t s, int* launches);
+
 // Records the launch count of an accepted call (read by kvzip_last_launch_count).
 void note_launches(int launches);
 
@@ -161,6 +215,7 @@ cudaError_t bounds_flag_select(unsigned int* out);
 cudaError_t bounds_flag_select_fused(unsigned int* out);
 cudaError_t bounds_flag_compact(unsigned int* out);
 cudaError_t bounds_flag_decode(unsigned int* out);
+cudaError_t bounds_flag_cache(unsigned int* out);
 
 // Scores are ranked by the bits of |s|: for s >= 0 the bit order is the value
 // order, and -0.0 ranks as 0.0 (its raw bits would rank above every score).

@@ -26,6 +26,16 @@ class KvzipError(RuntimeError):
         super().__init__(f"{where}: {status_string(status)} (status {status})")
 
 
+class CacheStruct(ctypes.Structure):
+    """kvzip_cache"""
+    _fields_ = [("format", ctypes.c_int32), ("d", ctypes.c_int32), ("page_rows", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("units", ctypes.c_int64), ("k_pages", ctypes.c_void_p),
+                ("v_pages", ctypes.c_void_p), ("k_params", ctypes.c_void_p),
+                ("v_params", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -35,6 +45,7 @@ def _load() -> ctypes.CDLL:
     vp, i32, i64, sz, f32, f64, u64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                        ctypes.c_size_t, ctypes.c_float, ctypes.c_double,
                                        ctypes.c_uint64)
+    cp = ctypes.POINTER(CacheStruct)
     sig = {
         "kvzip_score_workspace_size": (sz, [i32, i32, i32]),
         "kvzip_score_chunk": (i32, [i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, sz, vp]),
@@ -71,6 +82,11 @@ def _load() -> ctypes.CDLL:
         "kvzip_select_per_head": (i32, [vp, i64, i64, i64, vp, vp, vp, sz, vp]),
         "kvzip_decode_workspace_size": (sz, [i64, i32, i32]),
         "kvzip_decode_attention": (i32, [vp, vp, vp, i64, vp, i64, i32, i32, f32, vp, vp, sz, vp]),
+        "kvzip_cache_write": (i32, [cp, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp]),
+        "kvzip_cache_read": (i32, [cp, vp, vp, i64, vp, vp, vp]),
+        "kvzip_cache_attention_workspace_size": (sz, [cp, i32, i32]),
+        "kvzip_cache_attention": (i32, [cp, vp, i64, i64, i64, vp, i32, i64, i64, i64, vp, i32, i32,
+                                        f32, vp, sz, vp]),
         "kvzip_last_launch_count": (i32, []),
         "kvzip_debug_checks": (i32, []),
         "kvzip_debug_bounds_status": (i32, []),
@@ -498,6 +514,79 @@ def decode_attention(q: torch.Tensor, k_packed: torch.Tensor, v_packed: torch.Te
                                        workspace.numel(), _stream(stream)),
            "kvzip_decode_attention")
     return out
+
+
+# ---------------------------------------------------------------- paged cache
+
+CACHE_FORMATS = {"bf16": 0, "fp8": 1, "int4": 2}   # kvzip_cache_format
+
+
+def cache_row_bytes(fmt: str, d: int) -> int:
+    """Bytes of one stored row (without its parameter word)."""
+    return {"bf16": 2 * d, "fp8": d, "int4": d // 2}[fmt]
+
+
+def cache_struct(fmt: str, k_pages, v_pages, k_params, v_params, page_table, lens,
+                 status) -> CacheStruct:
+    """kvzip_cache over device tensors, which the caller keeps alive: pools
+    [n_pages][page_rows][d] bf16, or [n_pages][page_rows][row bytes] uint8 with
+    int32 [n_pages][page_rows] parameters; page_table int32 [units][max_pages];
+    lens int32 [units]; status int32 [1]."""
+    if fmt not in CACHE_FORMATS:
+        raise ValueError(f"cache format must be one of {sorted(CACHE_FORMATS)}, got {fmt!r}")
+    dt = torch.bfloat16 if fmt == "bf16" else torch.uint8
+    for n, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _dev_contig(n, t, dt)
+    if k_pages.dim() != 3 or k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must be [n_pages][page_rows][row], of one shape")
+    n_pages, page_rows, row = k_pages.shape
+    d = {"bf16": row, "fp8": row, "int4": 2 * row}[fmt]
+    if fmt != "bf16":
+        for n, t in (("k_params", k_params), ("v_params", v_params)):
+            if t is None:
+                raise ValueError(f"{n} is needed for {fmt}")
+            _dev_contig(n, t, torch.int32)
+            if t.shape != (n_pages, page_rows):
+                raise ValueError(f"{n} must be [n_pages][page_rows]")
+    for n, t in (("page_table", page_table), ("lens", lens), ("status", status)):
+        _dev_contig(n, t, torch.int32)
+    if page_table.dim() != 2 or lens.shape != (page_table.shape[0],) or status.numel() != 1:
+        raise ValueError("page_table must be [units][max_pages], lens [units], status [1]")
+    for t in (v_pages, k_params, v_params, page_table, lens, status):
+        if t is not None and t.device != k_pages.device:
+            raise ValueError("the cache's tensors must be on one device")
+    ptr = lambda t: None if t is None or fmt == "bf16" else t.data_ptr()  # noqa: E731
+    return CacheStruct(CACHE_FORMATS[fmt], d, page_rows, page_table.shape[1], n_pages,
+                       page_table.shape[0], k_pages.data_ptr(), v_pages.data_ptr(), ptr(k_params),
+                       ptr(v_params), page_table.data_ptr(), lens.data_ptr(), status.data_ptr())
+
+
+def cache_write(cache: CacheStruct, k, v, n_rows: int, k_strides, v_strides, starts=None,
+                counts=None, offsets=None, stream=None):
+    """kvzip_cache_write; k_strides / v_strides = (unit, row) strides in elements."""
+    _check(_lib.kvzip_cache_write(cache, _ptr(k), _ptr(v), *k_strides, *v_strides, n_rows,
+                                  _ptr(starts), _ptr(counts), _ptr(offsets), _stream(stream)),
+           "kvzip_cache_write")
+
+
+def cache_read(cache: CacheStruct, k_out, v_out, n_rows: int, starts=None, offsets=None,
+               stream=None):
+    """kvzip_cache_read"""
+    _check(_lib.kvzip_cache_read(cache, _ptr(k_out), _ptr(v_out), n_rows, _ptr(starts),
+                                 _ptr(offsets), _stream(stream)), "kvzip_cache_read")
+
+
+def cache_attention_workspace_size(cache: CacheStruct, G: int, n_q: int) -> int:
+    return int(_lib.kvzip_cache_attention_workspace_size(cache, G, n_q))
+
+
+def cache_attention(cache: CacheStruct, q, out, workspace, q_lens=None, scale: float = 0.0,
+                    stream=None):
+    """kvzip_cache_attention; q, out [units][G][n_q][d] (any strides, d contiguous)."""
+    _check(_lib.kvzip_cache_attention(
+        cache, _ptr(q), *q.stride()[:3], _ptr(out), int(out.dtype == torch.float32),
+        *out.stride()[:3], _ptr(q_lens), q.shape[2], q.shape[1], float(scale), _ptr(workspace),
+        workspace.numel(), _stream(stream)), "kvzip_cache_attention")
 
 
 def last_launch_count() -> int:

@@ -30,6 +30,7 @@
  *   - A failed launch returns KVZIP_ERR_CUDA.
  *   - Device pointers must be 16-byte aligned unless stated otherwise.
  *   - Calls that share a workspace must not overlap on the GPU.
+ *   - The current device must be the one the pointers and the stream belong to.
  */
 #ifndef KVZIP_H_
 #define KVZIP_H_
@@ -167,7 +168,8 @@ kvzip_status kvzip_score_lse_layout(int G, int n_in, size_t* offset_bytes, int64
  * leave in `workspace`: KVZIP_OK; KVZIP_ERR_TIMEOUT when a kernel abandoned a
  * pipeline or grid wait (its results for that call are then incomplete); or
  * KVZIP_ERR_INVALID_ARG when kvzip_select_hist found that its histogram does
- * not match the scores. */
+ * not match the scores, or a paged-cache call (given the cache's status word) met
+ * a length, count, offset or page id out of range. */
 kvzip_status kvzip_workspace_status(void* workspace, void* stream);
 
 /* Longest a scoring kernel waits on one pipeline stage before it gives up,
@@ -375,6 +377,134 @@ kvzip_status kvzip_decode_attention(const void* q, const void* k_packed, const v
                                     int64_t n_rows, const int64_t* offsets, int64_t n_heads,
                                     int G, int d, float scale, float* out, void* workspace,
                                     size_t ws_bytes, void* stream);
+
+/* -------------------------------------------------------- paged cache */
+
+/*
+ * A paged key/value cache that can grow, in 16, 8 or 4 bits an element.
+ *
+ * The packed cache of kvzip_compact cannot take new rows (the next head's rows
+ * follow at once), so a context's kept rows, the question's tokens and every
+ * generated token go into pages instead.  A unit is one KV head of one sequence;
+ * after eviction heads keep different numbers of rows, so every unit has its own
+ * length and its own list of pages.  The pages describe 4-bit KV caches as one of
+ * the method's combinations (Figure 10: KV4 quantisation, then eviction).
+ *
+ *   k_pages, v_pages    pools [n_pages][page_rows][row bytes]; a page holds
+ *                       page_rows consecutive rows of one unit.  16-byte aligned.
+ *   k_params, v_params  [n_pages][page_rows] uint32, one word a row (fp8, int4),
+ *                       16-byte aligned; NULL for bf16.
+ *   page_table          [units][max_pages] int32: row pos of unit u lies in page
+ *                       page_table[u][pos / page_rows], at pos % page_rows.
+ *                       Entries past a unit's last page are not read.
+ *   lens                [units] int32: rows each unit holds.
+ *   status              one sticky uint32 the kernels OR into; zero it before
+ *                       first use, read and clear it with kvzip_workspace_status.
+ *   page_rows           16, 32, 64 or 128.   d  128 or 256.
+ *   n_pages * page_rows and max_pages * page_rows are below 2^31.
+ *
+ * Row formats:
+ *   KVZIP_CACHE_BF16  2 d bytes.
+ *   KVZIP_CACHE_FP8   d e4m3 codes; parameter word = float32 scale 2^e with e the
+ *       smallest integer >= -126 for which max|x| <= 448 * 2^e (scale 1 for a row
+ *       of zeros); code = x / 2^e rounded to nearest even; value = code * 2^e,
+ *       exact in bf16.  A row with an infinity or NaN reads back as all NaN.
+ *   KVZIP_CACHE_INT4  d/2 bytes, element 2b in the low and 2b + 1 in the high half
+ *       of byte b; parameter word = bf16 s (low half) and bf16 z (high half).
+ *       z = min x, s = (max x - min x) / 15 rounded to bf16, code c = the integer
+ *       nearest (x - z) / s (ties to even; 0 where s = 0), held to 15; value =
+ *       s c + z.  A row with an infinity, a NaN or a magnitude of 2^126 or more
+ *       reads back as all NaN.
+ *
+ * A length, start, count or offset outside its range is held to it, a row whose
+ * page id lies outside the pool is neither read nor written (it attends as a row
+ * of zeros), and both are recorded: kvzip_workspace_status(status) then returns
+ * KVZIP_ERR_INVALID_ARG.  Nothing outside the caller's buffers is touched.
+ * Pages named by two units, or twice by one, may be read but not written.
+ */
+typedef enum {
+  KVZIP_CACHE_BF16 = 0,
+  KVZIP_CACHE_FP8 = 1,
+  KVZIP_CACHE_INT4 = 2
+} kvzip_cache_format;
+
+typedef struct {
+  int32_t format;              /* kvzip_cache_format */
+  int32_t d;
+  int32_t page_rows;
+  int32_t max_pages;
+  int64_t n_pages;
+  int64_t units;
+  void* k_pages;
+  void* v_pages;
+  uint32_t* k_params;
+  uint32_t* v_params;
+  const int32_t* page_table;
+  int32_t* lens;
+  uint32_t* status;
+} kvzip_cache;                 /* host struct of device pointers; calls do not keep it */
+
+/*
+ * Put rows of K and V into the cache, quantising them as they are written, and
+ * move the lengths on.
+ *
+ * Dense (offsets NULL): unit u brings counts[u] rows (n_rows where counts is
+ *   NULL; 0 <= counts[u] <= n_rows), row t at k + u * k_unit_stride + t *
+ *   k_row_stride, strides in elements (multiples of 8, zero allowed), d contiguous.
+ * Packed (offsets = [units + 1] int64, as kvzip_select and kvzip_compact give
+ *   them): unit u brings rows offsets[u] .. offsets[u + 1] - 1 of k and v, n_rows
+ *   rows in all, row r at k + r * k_row_stride; the unit strides and counts are
+ *   not used.
+ *
+ * Rows go to positions start + t, start = starts[u] (int32, device) or, where
+ * starts is NULL, lens[u] (append); lens[u] = start + rows brought.  starts may be
+ * lens itself (an append); otherwise the two must not overlap.  Rows past
+ * max_pages * page_rows are dropped and recorded in the status word.
+ *   k, v  bf16, 16-byte aligned (NULL only if n_rows is 0).
+ * One launch, or two for an append of packed rows or of more than 32 per unit.
+ */
+kvzip_status kvzip_cache_write(const kvzip_cache* cache, const void* k, const void* v,
+                               int64_t k_unit_stride, int64_t k_row_stride,
+                               int64_t v_unit_stride, int64_t v_row_stride, int64_t n_rows,
+                               const int32_t* starts, const int32_t* counts,
+                               const int64_t* offsets, void* stream);
+
+/*
+ * Read rows back as bf16 (the values of the formats above, rounded once).
+ * Dense (offsets NULL): k_out, v_out [units][n_rows][d], row t of unit u =
+ *   position start + t.  Packed: [n_rows][d], row offsets[u] + t.
+ * start = starts[u] or 0.  Rows at or past lens[u] (and rows of a page outside the
+ * pool) are left as they were.  Outputs 16-byte aligned.
+ */
+kvzip_status kvzip_cache_read(const kvzip_cache* cache, void* k_out, void* v_out, int64_t n_rows,
+                              const int32_t* starts, const int64_t* offsets, void* stream);
+
+/* Bytes of workspace kvzip_cache_attention needs (scratch; nothing is kept in
+ * it between calls and it needs no initialisation). */
+size_t kvzip_cache_attention_workspace_size(const kvzip_cache* cache, int G, int n_q);
+
+/*
+ * Attention of each unit's newest tokens over its cached rows, their own
+ * included: unit u has m = q_lens[u] new tokens (n_q where q_lens is NULL; 0 <= m
+ * <= n_q), whose K and V are its last m rows.  Token i of query head g sees rows
+ * j < lens[u] - m + i + 1:
+ *   out[u][g][i] = softmax_j(scale * q[u][g][i] . k_j) v_j,
+ * zeros where it sees nothing.  n_q = 1 is a decoding step.
+ *   q     bf16, element (u, g, i, e) at u * q_unit_stride + g * q_head_stride +
+ *         i * q_row_stride + e; strides in elements, multiples of 8 (zero allowed).
+ *   out   bf16 or, with out_f32 != 0, float32; strides likewise, positive along
+ *         dimensions larger than 1 and such that no two rows overlap.  Rows i >=
+ *         m are left as they were.
+ *   G     1 .. 64 query heads per unit; scale <= 0 or NaN selects 1/sqrt(d).
+ *   q, out 16-byte aligned; workspace 256-byte aligned.
+ * Logits and sums are held in float32.  Quantised caches are attended at their
+ * values s c + z or code * 2^e.
+ */
+kvzip_status kvzip_cache_attention(const kvzip_cache* cache, const void* q, int64_t q_unit_stride,
+                                   int64_t q_head_stride, int64_t q_row_stride, void* out,
+                                   int out_f32, int64_t out_unit_stride, int64_t out_head_stride,
+                                   int64_t out_row_stride, const int32_t* q_lens, int n_q, int G,
+                                   float scale, void* workspace, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------ variants */
 
