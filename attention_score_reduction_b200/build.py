@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libkvzip.so")
 LIB_DEBUG = os.path.join(HERE, "libkvzip_debug.so")   # with the device bounds checks
 SOURCES = ["kvzip_api.cu", "score_tc.cu", "score_simt.cu", "select.cu", "select_fused.cu", "compact.cu", "heads.cu", "decode.cu",
-           "cache.cu", "cache_attention.cu", "cache_attention_merge.cu"]
+           "cache.cu", "cache_attention.cu", "cache_attention_tc.cu", "cache_attention_merge.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

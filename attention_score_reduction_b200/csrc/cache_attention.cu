@@ -90,6 +90,8 @@ __device__ __forceinline__ uint32_t nib_f16x2(uint32_t w) {
     return hfma2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd400d400u);   // / 16 - 64
 }
 
+constexpr int kRowsTile = 64;     // cache rows of a tile: two or four batches, one per warp
+
 template <int FMT, int D>
 struct RowsCfg {
   static constexpr int WARPS = 4;
@@ -135,14 +137,14 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
 
   for (int64_t p = p0; p < p1; ++w) {
     const AttnItem it = attn_item(a.c, shape, w);
-    const int n_tiles = it.tiles();
+    const int n_tiles = it.n_tiles;
     const int64_t at = w_at;
     w_at += n_tiles;
     if (n_tiles == 0) continue;
     const int t0 = static_cast<int>(p - at);
     const int t1 = static_cast<int>(min(static_cast<int64_t>(n_tiles), p1 - at));
     p = at + t1;
-    const int r_end = min(t1 * kTileRows, it.vis);
+    const int r_end = min(t1 * kRowsTile, it.vis);
 
     // ---- query fragments and per-row limits (rows quad and quad + 8 of the item)
     uint32_t qa[KS][2 * NT];
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
     }
 
     // ---- batches of this warp: rows r0 + (warp + WARPS n) * BR
-    const int r_first = t0 * kTileRows + warp * BR;
+    const int r_first = t0 * kRowsTile + warp * BR;
     int64_t base[BR / 16];               // pool row of each 16-row group of the batch, or -1
     auto find = [&](int r) {
 #pragma unroll
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
         attn_store8(a, shape, it, row, e, v);
       }
     } else {
-      const int64_t slot = cta + w;
+      const int64_t slot = line_slot(all, cta, n_cta, at);
       for (int i = threadIdx.x; i < RQ * D / 4; i += THREADS)
         reinterpret_cast<float4*>(o_out + slot * RQ * D)[i] =
             reinterpret_cast<const float4*>(&xo[0][0][0])[i];
@@ -571,13 +573,12 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
 template <int FMT, int D, int NT>
 cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st, int* launches) {
   using Cfg = RowsCfg<FMT, D>;
-  AttnShape shape{a.q_lens, a.n_q, a.G, 8 * NT, 0};
-  shape.blocks = static_cast<int>((static_cast<int64_t>(a.n_q) * a.G + shape.block - 1) / shape.block);
+  const AttnShape shape = attn_shape(a.q_lens, a.n_q, a.G, 8 * NT, kRowsTile);
   const int64_t items = a.c.units * shape.blocks;
   const int ctas = rows_ctas(a.c.format, D);
   float2* ml = static_cast<float2*>(a.ws);
   float* o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) +
-                                      attn_ml_bytes((ctas + items) * shape.block));
+                                      attn_ml_bytes(ctas, shape.block));
   cache_attn_rows<FMT, D, NT><<<ctas, Cfg::THREADS, 0, st>>>(
       a, shape, items, a.scale * 1.4426950408889634f, ml, o);
   cudaError_t e = cudaGetLastError();
@@ -592,8 +593,10 @@ cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st, int* launches) 
 // allow three per SM, two for bf16 rows of 256).
 int rows_ctas(int format, int d) { return 148 * (format == kFmtBf16 && d == 256 ? 2 : 3); }
 
+int rows_block(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
 cudaError_t launch_cache_attn_rows(const CacheAttnArgs& a, cudaStream_t s, int* launches) {
-  const bool one = static_cast<int64_t>(a.n_q) * a.G <= 8;
+  const bool one = rows_block(static_cast<int64_t>(a.n_q) * a.G) == 8;
 #define KVZIP_ROWS(F, DD)                                            \
   case F * 1000 + DD:                                                \
     return one ? launch_rows<F, DD, 1>(a, s, launches) : launch_rows<F, DD, 2>(a, s, launches);

@@ -26,17 +26,33 @@ __device__ __forceinline__ void attn_store8(const CacheAttnArgs& a, const AttnSh
   }
 }
 
-inline size_t attn_ml_bytes(int64_t rows) {
-  return (static_cast<size_t>(rows) * sizeof(float2) + 255) / 256 * 256;
+inline AttnShape attn_shape(const int32_t* q_lens, int n_q, int G, int block, int tile) {
+  const int64_t rows = static_cast<int64_t>(n_q) * G;
+  return AttnShape{q_lens, n_q, G, block, static_cast<int>((rows + block - 1) / block), tile};
+}
+
+// Workspace: (m, l) of two slots per CTA, then their o rows.
+inline size_t attn_ml_bytes(int ctas, int block) {
+  return (2 * static_cast<size_t>(ctas) * block * sizeof(float2) + 255) / 256 * 256;
+}
+inline size_t attn_ws_bytes(int ctas, int block, int d) {
+  return attn_ml_bytes(ctas, block) + 2 * static_cast<size_t>(ctas) * block * d * sizeof(float);
 }
 
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the CTAs of each item
-// that no CTA covered whole; zeros for items (and rows) that see nothing.  Slot
-// cta + item holds shape.block rows of (m, l) and of o[d].
+// that no CTA covered whole; zeros for items (and rows) that see nothing.  A
+// slot holds shape.block rows of (m, l), m in the log2 domain, and of o[d].
 cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, int64_t items,
                               int ctas, const float2* ml, const float* o, cudaStream_t st);
 
+// Few query rows a unit: mma.sync, straight from global memory.
 int rows_ctas(int format, int d);
+int rows_block(int64_t rows);      // query rows of an item, for `rows` rows a unit
 cudaError_t launch_cache_attn_rows(const CacheAttnArgs& a, cudaStream_t s, int* launches);
+
+// Many: tcgen05, one CTA per SM.
+constexpr int kTcCtas = 148;
+int tc_block(int d);
+cudaError_t launch_cache_attn_tc(const CacheAttnArgs& a, cudaStream_t s, int* launches);
 
 }  // namespace kvzip

@@ -28,14 +28,16 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int64_t w = blockIdx.x;
   const AttnItem it = attn_item(a.c, shape, w);
   if (it.rows <= 0 || static_cast<int>(blockIdx.y) >= it.rows) return;
-  const int n_tiles = it.tiles();
+  const int n_tiles = it.n_tiles;
   int64_t c0 = 0, c1 = 0;                // CTAs with a part of the item, inclusive
+  int64_t slot0 = 0;                     // slot of c0's part; later CTAs begin with the item
   if (n_tiles > 0) {
     const LineTotals t = line_totals<kMergeThreads>(a.c, shape, items, w, scratch);
     const int64_t n = line_ctas(t.all, ctas);
     c0 = line_cta(t.all, t.before, n);
     c1 = line_cta(t.all, t.before + n_tiles - 1, n);
     if (c0 == c1) return;                // one CTA wrote the output itself
+    slot0 = line_slot(t.all, c0, n, t.before);
   }
   const int col = threadIdx.x % COLS, grp = threadIdx.x / COLS;
   for (int row = blockIdx.y; row < it.rows; row += gridDim.y) {
@@ -43,11 +45,11 @@ __global__ void __launch_bounds__(kMergeThreads)
     float l = 0.f;
     if (n_tiles > 0) {
       float M = -INFINITY;
-      for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, ml[(c + w) * shape.block + row].x);
+      for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, ml[(c == c0 ? slot0 : 2 * c) * shape.block + row].x);
       const float sub = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
       for (int64_t c = c0 + grp; c <= c1; c += GROUPS) {
-        const int64_t slot = (c + w) * shape.block + row;
+        const int64_t slot = (c == c0 ? slot0 : 2 * c) * shape.block + row;
         const float2 v = ml[slot];
         const float f = exp2f(v.x - sub);
         const float4 x = reinterpret_cast<const float4*>(o + slot * D)[col];
@@ -101,15 +103,20 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
              : cudaLaunchKernelEx(&cfg, cache_attn_merge<256>, a, shape, items, ctas, ml, o);
 }
 
+// Up to 16 query rows a unit go to the mma.sync kernel, which reads the cache once
+// for them; beyond, the tensor-memory kernel, whose tiles hold 128.
+static bool few_rows(int n_q, int G) { return static_cast<int64_t>(n_q) * G <= 16; }
+
 size_t cache_attn_ws_bytes(int64_t units, int G, int n_q, int d, int format) {
-  const int64_t rows = static_cast<int64_t>(n_q) * G;
-  const int64_t block = rows <= 8 ? 8 : 16;
-  const int64_t slots = (rows_ctas(format, d) + units * ((rows + block - 1) / block)) * block;
-  return attn_ml_bytes(slots) + static_cast<size_t>(slots) * d * sizeof(float);
+  (void)units;
+  return few_rows(n_q, G)
+             ? attn_ws_bytes(rows_ctas(format, d), rows_block(static_cast<int64_t>(n_q) * G), d)
+             : attn_ws_bytes(kTcCtas, tc_block(d), d);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t s, int* launches) {
-  return launch_cache_attn_rows(a, s, launches);
+  return few_rows(a.n_q, a.G) ? launch_cache_attn_rows(a, s, launches)
+                              : launch_cache_attn_tc(a, s, launches);
 }
 
 }  // namespace kvzip

@@ -1,13 +1,13 @@
 // How the attention kernels over the paged cache share their work.
 //
-// An item is one unit's block of query rows.  Its work is the 64-row tiles of
-// the cache its last row can see.  Heads keep very different numbers of rows
+// An item is one unit's block of query rows.  Its work is the tiles of cache
+// rows its last row can see.  Heads keep very different numbers of rows
 // after eviction, so the items' tiles are laid end to end on one line and every
 // CTA takes an equal piece of it, crossing items where it must (a fixed number of
 // splits per head would wait for the longest head).  Lengths live on the device;
 // every CTA adds them up itself.  A CTA's part of an item that it does not cover
-// whole is a partial result in slot cta + item: slots never collide, because
-// along the line every new part raises cta or item.
+// whole is a partial result; a CTA has at most two, of its first and its last
+// item, in slots 2 cta and 2 cta + 1.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -17,13 +17,12 @@
 
 namespace kvzip {
 
-constexpr int kTileRows = 64;    // rows of one unit of work
-
 struct AttnShape {
   const int32_t* q_lens;
   int n_q, G;
   int block;       // query rows of one item; row r of a unit is token r / G, head r % G
   int blocks;      // items per unit
+  int tile;        // cache rows of one tile
 };
 
 struct AttnItem {
@@ -32,7 +31,7 @@ struct AttnItem {
   int m;           // its new tokens
   int row0, rows;  // query rows [row0, row0 + rows)
   int vis;         // cache rows the item's last query row sees
-  __device__ int tiles() const { return (vis + kTileRows - 1) / kTileRows; }
+  int n_tiles;
 };
 
 // Cache rows that token i sees (may be negative: none).
@@ -48,6 +47,7 @@ __device__ __forceinline__ AttnItem attn_item(const CacheArgs& c, const AttnShap
   it.rows = min(s.block, it.m * s.G - it.row0);
   it.vis = 0;
   if (it.rows > 0) it.vis = max(0, seen_rows(it, (it.row0 + it.rows - 1) / s.G));
+  it.n_tiles = (it.vis + s.tile - 1) / s.tile;
   return it;
 }
 
@@ -74,7 +74,7 @@ __device__ __forceinline__ LineTotals line_totals(const CacheArgs& c, const Attn
                                                   int64_t items, int64_t w, int64_t* scratch) {
   int64_t all = 0, before = 0;
   for (int64_t i = threadIdx.x; i < items; i += THREADS) {
-    const int t = attn_item(c, s, i).tiles();
+    const int t = attn_item(c, s, i).n_tiles;
     all += t;
     if (i < w) before += t;
   }
@@ -93,7 +93,7 @@ __device__ __forceinline__ void line_find(const CacheArgs& c, const AttnShape& s
   int64_t base = 0;
   for (int64_t i0 = 0; i0 < items; i0 += THREADS) {
     const int64_t i = i0 + threadIdx.x;
-    const int t = i < items ? attn_item(c, s, i).tiles() : 0;
+    const int t = i < items ? attn_item(c, s, i).n_tiles : 0;
     int64_t inc = t;
 #pragma unroll
     for (int w = 1; w < 32; w <<= 1) {
@@ -131,6 +131,10 @@ __device__ __forceinline__ int64_t line_ctas(int64_t all, int64_t grid) {
 // Piece of the line that CTA i of n takes: [line_cut(i), line_cut(i + 1)).
 __device__ __forceinline__ int64_t line_cut(int64_t all, int64_t i, int64_t n) {
   return all * i / n;
+}
+// Slot of CTA i's part of the item whose tiles begin at `before` on the line.
+__device__ __forceinline__ int64_t line_slot(int64_t all, int64_t i, int64_t n, int64_t before) {
+  return 2 * i + (line_cut(all, i, n) >= before ? 0 : 1);
 }
 // The CTA that takes tile p.
 __device__ __forceinline__ int64_t line_cta(int64_t all, int64_t p, int64_t n) {

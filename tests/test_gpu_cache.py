@@ -375,7 +375,7 @@ def check_attention(c, q, out, lens, q_lens, scale=None, untouched=None):
 
 
 def uses_tensor_memory(G, n_q):
-    return False
+    return G * n_q > 16
 
 
 def filled(kc, fmt, lens, d, page_rows, seed, capacity=None):
