@@ -128,12 +128,13 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
   const int64_t cta = blockIdx.x;
 
   cudaTriggerProgrammaticLaunchCompletion();   // the merge may be launched; it waits for this grid
-  const int64_t all = line_totals<THREADS>(a.c, shape, items, 0, scratch).all;
+  Line<THREADS> line(a.c, shape, items, scratch, found);
+  const int64_t all = line.all;
   const int64_t n_cta = line_ctas(all, gridDim.x);
   if (cta >= n_cta) return;
   const int64_t p0 = line_cut(all, cta, n_cta), p1 = line_cut(all, cta + 1, n_cta);
   int64_t w, w_at;
-  line_find<THREADS>(a.c, shape, items, p0, &w, &w_at, scratch, found);
+  line.find(p0, &w, &w_at);
 
   for (int64_t p = p0; p < p1; ++w) {
     const AttnItem it = attn_item(a.c, shape, w);

@@ -2,83 +2,164 @@
 // workspace they live in.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "cache_attention.cuh"
 #include "kvzip_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace kvzip {
 
 namespace {
 
 constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kWarpSplits = 8;      // up to this many parts a warp joins a row alone
 
-// Block (item, y) merges rows y, y + gridDim.y, ... of the item.  The threads
-// are D / 4 columns of four elements by 1024 / D groups of splits, so the loads of
-// a row's splits are in flight together; groups meet in shared memory.
+// One row's elements as a warp holds them: lane * 4 + 128 i.
+template <int D>
+struct RowPart {
+  float4 v[D / 128];
+};
+
+template <int D>
+__device__ __forceinline__ void add_part(RowPart<D>& acc, const float* o, float f) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < D / 128; ++i) {
+    const float4 x = reinterpret_cast<const float4*>(o)[lane + 32 * i];
+    acc.v[i].x = fmaf(x.x, f, acc.v[i].x);
+    acc.v[i].y = fmaf(x.y, f, acc.v[i].y);
+    acc.v[i].z = fmaf(x.z, f, acc.v[i].z);
+    acc.v[i].w = fmaf(x.w, f, acc.v[i].w);
+  }
+}
+
+// out row = acc / L (0 where L is 0), four elements a lane.
+template <int D>
+__device__ __forceinline__ void put_row(const CacheAttnArgs& a, const AttnShape& s,
+                                        const AttnItem& it, int row, const RowPart<D>& acc, float L) {
+  const int lane = threadIdx.x & 31;
+  const int r = it.row0 + row, tok = r / s.G, g = r - tok * s.G;
+  const int64_t at = it.u * a.o_unit + g * a.o_head + tok * a.o_row + 4 * lane;
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+#pragma unroll
+  for (int i = 0; i < D / 128; ++i) {
+    float4 x = acc.v[i];
+    x = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                 : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (a.out_f32)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 128 * i) = x;
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 128 * i) =
+          make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+  }
+}
+
+// Which item a block joins does not depend on the results, so it is found before
+// the wait for the grid that computes them.  Blocks are one per item, or (many
+// items: few of them are split) one per cut between two CTAs, of which the first
+// inside an item serves it.  Items with few parts (a long chunk: two or three)
+// give a row to each warp; with many (one token: dozens) the warps of a block
+// share a row's parts, so that their loads are in flight together.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     cache_attn_merge(const CacheAttnArgs a, const AttnShape shape, int64_t items, int ctas,
-                     const float2* __restrict__ ml, const float* __restrict__ o) {
-  constexpr int COLS = D / 4, GROUPS = kMergeThreads / COLS;
-  __shared__ int64_t scratch[kMergeThreads / 32];
-  __shared__ float4 acc_s[GROUPS][COLS];
-  __shared__ float l_s[GROUPS];
-  cudaGridDependencySynchronize();       // the partial results are complete and visible
-  const int64_t w = blockIdx.x;
-  const AttnItem it = attn_item(a.c, shape, w);
-  if (it.rows <= 0 || static_cast<int>(blockIdx.y) >= it.rows) return;
-  const int n_tiles = it.n_tiles;
+                     int by_item, const float2* __restrict__ ml, const float* __restrict__ o) {
+  __shared__ int64_t scratch[kMergeWarps];
+  __shared__ int64_t found[2];
+  __shared__ RowPart<D> acc_s[kMergeWarps][32];
+  __shared__ float l_s[kMergeWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int64_t w = blockIdx.x, before = 0;
+  bool split = false;
   int64_t c0 = 0, c1 = 0;                // CTAs with a part of the item, inclusive
-  int64_t slot0 = 0;                     // slot of c0's part; later CTAs begin with the item
-  if (n_tiles > 0) {
-    const LineTotals t = line_totals<kMergeThreads>(a.c, shape, items, w, scratch);
-    const int64_t n = line_ctas(t.all, ctas);
-    c0 = line_cta(t.all, t.before, n);
-    c1 = line_cta(t.all, t.before + n_tiles - 1, n);
-    if (c0 == c1) return;                // one CTA wrote the output itself
-    slot0 = line_slot(t.all, c0, n, t.before);
+  Line<kMergeThreads> t(a.c, shape, items, scratch, found);
+  const int64_t n = line_ctas(t.all, ctas);
+  if (by_item) {
+    before = t.before(w);
+  } else if (w + 1 < n) {
+    const int64_t cut = line_cut(t.all, w + 1, n);
+    const int64_t last = line_cut(t.all, w, n);
+    t.find(cut, &w, &before);
+    split = before < cut && last <= before;          // the first cut inside item w
   }
-  const int col = threadIdx.x % COLS, grp = threadIdx.x / COLS;
-  for (int row = blockIdx.y; row < it.rows; row += gridDim.y) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    if (n_tiles > 0) {
-      float M = -INFINITY;
-      for (int64_t c = c0; c <= c1; ++c) M = fmaxf(M, ml[(c == c0 ? slot0 : 2 * c) * shape.block + row].x);
-      const float sub = M == -INFINITY ? 0.f : M;
+  const AttnItem it = attn_item(a.c, shape, by_item || split ? w : 0);
+  if (by_item || split) {
+    if (it.n_tiles > 0) {
+      c0 = line_cta(t.all, before, n);
+      c1 = line_cta(t.all, before + it.n_tiles - 1, n);
+    }
+    split = c0 != c1;
+  }
+  cudaGridDependencySynchronize();       // the partial results are complete and visible
+
+  if (split) {
+    const int parts = static_cast<int>(c1 - c0) + 1;
+    const int64_t slot0 = line_slot(t.all, c0, n, before);     // later CTAs begin with the item
+    auto part = [&](int i) { return (i == 0 ? slot0 : 2 * (c0 + i)) * shape.block; };
+    if (parts <= kWarpSplits) {
+      for (int row = blockIdx.y * kMergeWarps + warp; row < it.rows; row += gridDim.y * kMergeWarps) {
+        const float2 x = lane < parts ? ml[part(lane) + row] : make_float2(-INFINITY, 0.f);
+        float M = x.x;
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, k));
+        const float f = exp2f(x.x - (M == -INFINITY ? 0.f : M));
+        float L = lane < parts ? x.y * f : 0.f;
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) L += __shfl_xor_sync(0xffffffffu, L, k);
+        RowPart<D> acc = {};
 #pragma unroll 4
-      for (int64_t c = c0 + grp; c <= c1; c += GROUPS) {
-        const int64_t slot = (c == c0 ? slot0 : 2 * c) * shape.block + row;
-        const float2 v = ml[slot];
-        const float f = exp2f(v.x - sub);
-        const float4 x = reinterpret_cast<const float4*>(o + slot * D)[col];
-        l = fmaf(v.y, f, l);
-        acc.x = fmaf(x.x, f, acc.x);
-        acc.y = fmaf(x.y, f, acc.y);
-        acc.z = fmaf(x.z, f, acc.z);
-        acc.w = fmaf(x.w, f, acc.w);
+        for (int i = 0; i < parts; ++i)
+          add_part<D>(acc, o + (part(i) + row) * D, __shfl_sync(0xffffffffu, f, i));
+        put_row<D>(a, shape, it, row, acc, L);
+      }
+    } else {
+      for (int row = blockIdx.y; row < it.rows; row += gridDim.y) {
+        float M = -INFINITY;
+        for (int i = lane; i < parts; i += 32) M = fmax_nan(M, ml[part(i) + row].x);
+#pragma unroll
+        for (int k = 16; k >= 1; k >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, k));
+        const float sub = M == -INFINITY ? 0.f : M;
+        RowPart<D> acc = {};
+        float L = 0.f;
+#pragma unroll 4
+        for (int i = warp; i < parts; i += kMergeWarps) {
+          const float2 x = ml[part(i) + row];
+          const float f = exp2f(x.x - sub);
+          L = fmaf(x.y, f, L);
+          add_part<D>(acc, o + (part(i) + row) * D, f);
+        }
+        acc_s[warp][lane] = acc;
+        if (lane == 0) l_s[warp] = L;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+          for (int k = 1; k < kMergeWarps; ++k) {
+            const RowPart<D> x = acc_s[k][lane];
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i) {
+              acc.v[i].x += x.v[i].x;
+              acc.v[i].y += x.v[i].y;
+              acc.v[i].z += x.v[i].z;
+              acc.v[i].w += x.v[i].w;
+            }
+            L += l_s[k];
+          }
+          put_row<D>(a, shape, it, row, acc, L);
+        }
+        __syncthreads();
       }
     }
-    acc_s[grp][col] = acc;
-    if (col == 0) l_s[grp] = l;
-    __syncthreads();
-    if (threadIdx.x < D / 8) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      float L = 0.f;
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g) {
-        const float4 x = acc_s[g][2 * threadIdx.x], y = acc_s[g][2 * threadIdx.x + 1];
-        v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
-        v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
-        L += l_s[g];
-      }
-      const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = L == 0.f ? 0.f : v[k] * inv;
-      attn_store8(a, shape, it, row, 8 * threadIdx.x, v);
-    }
-    __syncthreads();
+  }
+  // items that see nothing: zeros
+  const RowPart<D> zero = {};
+  for (int64_t z = blockIdx.x; z < items; z += gridDim.x) {
+    const AttnItem iz = attn_item(a.c, shape, z);
+    if (iz.n_tiles == 0)
+      for (int row = blockIdx.y * kMergeWarps + warp; row < iz.rows; row += gridDim.y * kMergeWarps)
+        put_row<D>(a, shape, iz, row, zero, 0.f);
   }
 }
 
@@ -86,11 +167,13 @@ __global__ void __launch_bounds__(kMergeThreads)
 
 cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, int64_t items,
                               int ctas, const float2* ml, const float* o, cudaStream_t st) {
-  // enough blocks to fill the machine, rows of an item shared by several
-  int64_t y = (148 * 8 + items - 1) / items;
-  if (y > shape.block) y = shape.block;
+  // y: blocks that share an item's rows, a row or eight at a time
+  const int by_item = items <= ctas;
+  const int64_t x = by_item ? items : ctas;
+  const int64_t y = by_item ? std::min<int64_t>(shape.block, std::max<int64_t>(1, 148 * 8 / x))
+                            : 148 * 8 / x;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(items), static_cast<unsigned>(y));
+  cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -98,9 +181,10 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return a.c.d == 128
-             ? cudaLaunchKernelEx(&cfg, cache_attn_merge<128>, a, shape, items, ctas, ml, o)
-             : cudaLaunchKernelEx(&cfg, cache_attn_merge<256>, a, shape, items, ctas, ml, o);
+  return a.c.d == 128 ? cudaLaunchKernelEx(&cfg, cache_attn_merge<128>, a, shape, items, ctas,
+                                           by_item, ml, o)
+                      : cudaLaunchKernelEx(&cfg, cache_attn_merge<256>, a, shape, items, ctas,
+                                           by_item, ml, o);
 }
 
 // Up to 16 query rows a unit go to the mma.sync kernel, which reads the cache once

@@ -39,7 +39,7 @@ __device__ __forceinline__ int seen_rows(const AttnItem& it, int i) { return it.
 
 __device__ __forceinline__ AttnItem attn_item(const CacheArgs& c, const AttnShape& s, int64_t w) {
   AttnItem it;
-  it.u = w / s.blocks;
+  it.u = static_cast<uint32_t>(w) / static_cast<uint32_t>(s.blocks);   // w < 2^31
   const int b = static_cast<int>(w - it.u * s.blocks);
   it.len = held_to(c.lens[it.u], cache_cap(c), c.status);
   it.m = s.q_lens ? held_to(s.q_lens[it.u], s.n_q, c.status) : s.n_q;
@@ -51,77 +51,98 @@ __device__ __forceinline__ AttnItem attn_item(const CacheArgs& c, const AttnShap
   return it;
 }
 
-// Sum of v over the block (THREADS threads, all of them); scratch: THREADS / 32 entries.
+// The line as the THREADS threads of a block see it: `sums` (THREADS / 32 entries)
+// and `found` (2) are shared scratch.  Up to THREADS items are loaded once, one per
+// thread; more are walked again for every question.
 template <int THREADS>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* scratch) {
-#pragma unroll
-  for (int w = 16; w >= 1; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  int64_t t = 0;
-#pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) t += scratch[i];
-  return t;
-}
+struct Line {
+  const CacheArgs& c;
+  const AttnShape& s;
+  int64_t items;
+  int64_t* sums;
+  int64_t* found;
+  int64_t all;         // tiles of all items
+  int64_t mine_end;    // items <= THREADS: tiles up to and with item threadIdx.x
+  int mine;            // its own
 
-// Tiles of all items, and of the items before item w.
-struct LineTotals {
-  int64_t all, before;
-};
-template <int THREADS>
-__device__ __forceinline__ LineTotals line_totals(const CacheArgs& c, const AttnShape& s,
-                                                  int64_t items, int64_t w, int64_t* scratch) {
-  int64_t all = 0, before = 0;
-  for (int64_t i = threadIdx.x; i < items; i += THREADS) {
-    const int t = attn_item(c, s, i).n_tiles;
-    all += t;
-    if (i < w) before += t;
+  __device__ Line(const CacheArgs& c_, const AttnShape& s_, int64_t items_, int64_t* sums_,
+                  int64_t* found_)
+      : c(c_), s(s_), items(items_), sums(sums_), found(found_), all(0), mine_end(0), mine(0) {
+    if (items <= THREADS) {
+      mine = threadIdx.x < items ? attn_item(c, s, threadIdx.x).n_tiles : 0;
+      mine_end = scan(mine, &all);
+    } else {
+      int64_t v = 0;
+      for (int64_t i = threadIdx.x; i < items; i += THREADS) v += attn_item(c, s, i).n_tiles;
+      scan(v, &all);
+    }
   }
-  LineTotals r;
-  r.all = block_sum<THREADS>(all, scratch);
-  r.before = block_sum<THREADS>(before, scratch);
-  return r;
-}
 
-// The item that holds tile p of the line (0 <= p < all) and its first tile's place.
-template <int THREADS>
-__device__ __forceinline__ void line_find(const CacheArgs& c, const AttnShape& s, int64_t items,
-                                          int64_t p, int64_t* item, int64_t* item_at,
-                                          int64_t* scratch, int64_t* found) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t base = 0;
-  for (int64_t i0 = 0; i0 < items; i0 += THREADS) {
-    const int64_t i = i0 + threadIdx.x;
-    const int t = i < items ? attn_item(c, s, i).n_tiles : 0;
-    int64_t inc = t;
+  // Inclusive prefix sum over the block's threads, and the total.
+  __device__ int64_t scan(int64_t v, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int w = 1; w < 32; w <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, inc, w);
-      if (lane >= w) inc += o;
+    for (int k = 1; k < 32; k <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, v, k);
+      if (lane >= k) v += o;
     }
     __syncthreads();
-    if (lane == 31) scratch[warp] = inc;
+    if (lane == 31) sums[warp] = v;
     __syncthreads();
-    int64_t off = base;
-    int64_t sum = 0;
+    int64_t t = 0;
 #pragma unroll
     for (int k = 0; k < THREADS / 32; ++k) {
-      if (k < warp) off += scratch[k];
-      sum += scratch[k];
+      if (k < warp) v += sums[k];
+      t += sums[k];
     }
-    if (t > 0 && off + inc - t <= p && p < off + inc) {
-      found[0] = i;
-      found[1] = off + inc - t;
-    }
-    base += sum;
-    if (base > p) break;      // the same for every thread
+    *total = t;
+    return v;
   }
-  __syncthreads();
-  *item = found[0];
-  *item_at = found[1];
-  __syncthreads();
-}
+
+  // The item that holds tile p (0 <= p < all) and the place of its first tile.
+  __device__ void find(int64_t p, int64_t* item, int64_t* at) {
+    if (items <= THREADS) {
+      if (mine > 0 && mine_end - mine <= p && p < mine_end) {
+        found[0] = threadIdx.x;
+        found[1] = mine_end - mine;
+      }
+    } else {
+      int64_t base = 0;
+      for (int64_t i0 = 0; i0 < items; i0 += THREADS) {
+        const int64_t i = i0 + threadIdx.x;
+        const int t = i < items ? attn_item(c, s, i).n_tiles : 0;
+        int64_t sum;
+        const int64_t end = base + scan(t, &sum);
+        if (t > 0 && end - t <= p && p < end) {
+          found[0] = i;
+          found[1] = end - t;
+        }
+        base += sum;
+        if (base > p) break;      // the same for every thread
+      }
+    }
+    __syncthreads();
+    *item = found[0];
+    *at = found[1];
+    __syncthreads();
+  }
+
+  // Tiles before item w.
+  __device__ int64_t before(int64_t w) {
+    if (items <= THREADS) {
+      if (threadIdx.x == w) found[0] = mine_end - mine;
+    } else {
+      int64_t v = 0, sum;
+      for (int64_t i = threadIdx.x; i < w; i += THREADS) v += attn_item(c, s, i).n_tiles;
+      scan(v, &sum);
+      if (threadIdx.x == 0) found[0] = sum;
+    }
+    __syncthreads();
+    const int64_t r = found[0];
+    __syncthreads();
+    return r;
+  }
+};
 
 // CTAs with work: no more than there are tiles, so that every one's piece holds
 // at least one tile and every slot between an item's first and last CTA is written.
