@@ -40,6 +40,7 @@ class PagedCache:
         self._c = kz.cache_struct(fmt, k_pages, v_pages, k_params, v_params, page_table, lens,
                                   status)
         self.device = k_pages.device
+        self._index = self.device.index
         self.units, self.d = int(self._c.units), int(self._c.d)
         self.page_rows, self.n_pages = int(self._c.page_rows), int(self._c.n_pages)
         self.max_pages = int(self._c.max_pages)
@@ -109,26 +110,38 @@ class PagedCache:
         call allocates belongs to the stream that uses it."""
         with torch.cuda.device(self.device):
             if stream is None:
-                yield torch.cuda.current_stream(self.device)
+                yield torch.cuda.current_stream(self.device).cuda_stream
             else:
                 with torch.cuda.stream(stream):
-                    yield stream
+                    yield stream.cuda_stream
+
+    def _run(self, stream, call, *args):
+        """call(*args, raw stream) on the cache's device and the given stream.  The
+        usual case, both current already, costs no context switches: a decoding
+        step's calls are short enough for the host's time to show."""
+        if stream is None and torch.cuda.current_device() == self._index:
+            return call(*args, torch.cuda.current_stream(self._index).cuda_stream)
+        with self._on(stream) as st:
+            return call(*args, st)
 
     def _aux(self, name, t, dtype, n):
         if t is None:
             return
+        if t.dtype is dtype and t.device == self.device and t.shape == (n,) and t.is_contiguous():
+            return
         kz._dev_contig(name, t, dtype)
-        if t.device != self.device or t.shape != (n,):
-            raise ValueError(f"{name} must hold {n} numbers on {self.device}")
+        raise ValueError(f"{name} must hold {n} numbers on {self.device}")
 
     def _rows(self, name, t, dims):
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
         if t.device != self.device:
             raise ValueError(f"{name} must be on {self.device}")
-        if t.dim() != dims or t.shape[-1] != self.d or (t.numel() and t.stride(-1) != 1):
+        shape = t.shape
+        if len(shape) != dims or shape[-1] != self.d or (t.stride(-1) != 1 and t.numel()):
             raise ValueError(f"{name} must have {dims} dimensions, the last of {self.d} "
                              "contiguous elements")
+        return shape
 
     def write(self, k, v, starts=None, counts=None, offsets=None, stream=None):
         """Rows into the cache, at positions ``starts`` (int32 [units]; None:
@@ -140,22 +153,19 @@ class PagedCache:
         offsets[u]:offsets[u + 1].
         """
         dims = 2 if offsets is not None else 3
-        self._rows("k", k, dims)
-        self._rows("v", v, dims)
-        if k.shape != v.shape:
+        shape = self._rows("k", k, dims)
+        if self._rows("v", v, dims) != shape:
             raise ValueError("k and v must have the same shape")
-        if dims == 3 and k.shape[0] != self.units:
+        if dims == 3 and shape[0] != self.units:
             raise ValueError("k and v must hold every unit")
         if offsets is not None and counts is not None:
             raise ValueError("counts go with dense rows, offsets with packed ones")
         self._aux("starts", starts, torch.int32, self.units)
         self._aux("counts", counts, torch.int32, self.units)
         self._aux("offsets", offsets, torch.int64, self.units + 1)
-        ks, vs = k.stride()[:-1], v.stride()[:-1]
-        if dims == 2:
-            ks, vs = (0, ks[0]), (0, vs[0])
-        with self._on(stream) as st:
-            kz.cache_write(self._c, k, v, k.shape[-2], ks, vs, starts, counts, offsets, st)
+        ks, vs = k.stride(), v.stride()
+        ks, vs = ((0, ks[0]), (0, vs[0])) if dims == 2 else (ks[:2], vs[:2])
+        self._run(stream, kz.cache_write, self._c, k, v, shape[-2], ks, vs, starts, counts, offsets)
 
     def read(self, offsets=None, n_rows: int | None = None, starts=None, k_out=None, v_out=None,
              stream=None):
@@ -170,18 +180,21 @@ class PagedCache:
         self._aux("starts", starts, torch.int32, self.units)
         self._aux("offsets", offsets, torch.int64, self.units + 1)
         shape = (n_rows, self.d) if offsets is not None else (self.units, n_rows, self.d)
-        with self._on(stream) as st:
-            outs = []
-            for name, t in (("k_out", k_out), ("v_out", v_out)):
-                if t is None:
-                    make = torch.zeros if offsets is None else torch.empty
-                    t = make(shape, dtype=torch.bfloat16, device=self.device)
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None:
                 kz._dev_contig(name, t, torch.bfloat16)
                 if t.shape != shape or t.device != self.device:
                     raise ValueError(f"{name} must be {shape} on {self.device}")
-                outs.append(t)
-            kz.cache_read(self._c, outs[0], outs[1], n_rows, starts, offsets, st)
-        return outs[0], outs[1]
+        return self._run(stream, self._read, shape, n_rows, starts, offsets, k_out, v_out)
+
+    def _read(self, shape, n_rows, starts, offsets, k_out, v_out, st):
+        make = torch.zeros if offsets is None else torch.empty
+        if k_out is None:
+            k_out = make(shape, dtype=torch.bfloat16, device=self.device)
+        if v_out is None:
+            v_out = make(shape, dtype=torch.bfloat16, device=self.device)
+        kz.cache_read(self._c, k_out, v_out, n_rows, starts, offsets, st)
+        return k_out, v_out
 
     def attend(self, q, q_lens=None, out=None, scale: float = 0.0, out_dtype=torch.bfloat16,
                stream=None):
@@ -191,33 +204,36 @@ class PagedCache:
         Returns out [units][G][n_q][d] bf16 or float32; rows past q_lens[u] are
         left as they were (fresh outputs: zeros).
         """
-        self._rows("q", q, 4)
-        if q.shape[0] != self.units:
+        shape = self._rows("q", q, 4)
+        if shape[0] != self.units:
             raise ValueError("q must hold every unit")
         self._aux("q_lens", q_lens, torch.int32, self.units)
-        with self._on(stream) as st:
-            if out is None:
-                make = torch.empty if q_lens is None else torch.zeros
-                out = make(q.shape, dtype=out_dtype, device=self.device)
-            elif out.shape != q.shape or out.device != self.device or (
+        if out is not None:
+            if out.shape != shape or out.device != self.device or (
                     out.dtype not in (torch.bfloat16, torch.float32)):
-                raise ValueError(f"out must be bf16 or float32 {tuple(q.shape)} on {self.device}")
-            elif out.numel() and not _rows_apart(out):
+                raise ValueError(f"out must be bf16 or float32 {tuple(shape)} on {self.device}")
+            if not out.is_contiguous() and not _rows_apart(out):
                 raise ValueError("out's last dimension must be contiguous and its rows apart")
-            key = (q.shape[1], q.shape[2])
-            n = self._ws_sizes.get(key)
-            if n is None:
-                n = self._ws_sizes[key] = kz.cache_attention_workspace_size(self._c, *key)
-            # scratch of this call alone: two captured graphs never share it
-            ws = torch.empty(max(n, 256), dtype=torch.uint8, device=self.device)
-            kz.cache_attention(self._c, q, out, ws, q_lens, scale, st)
+        return self._run(stream, self._attend, q, q_lens, out, out_dtype, scale)
+
+    def _attend(self, q, q_lens, out, out_dtype, scale, st):
+        if out is None:
+            make = torch.empty if q_lens is None else torch.zeros
+            out = make(q.shape, dtype=out_dtype, device=self.device)
+        key = (q.shape[1], q.shape[2])
+        n = self._ws_sizes.get(key)
+        if n is None:
+            n = self._ws_sizes[key] = max(
+                kz.cache_attention_workspace_size(self._c, *key), 256)
+        # scratch of this call alone: two captured graphs never share it
+        ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        kz.cache_attention(self._c, q, out, ws, q_lens, scale, st)
         return out
 
     def check_status(self, stream=None):
         """Synchronise; raise if a call since the last check met a length, count,
         offset or page id out of range, or a kernel gave up waiting."""
-        with self._on(stream) as st:
-            s = kz.workspace_status(self.status, st)
+        s = self._run(stream, kz.workspace_status, self.status)
         if s != kz.OK:
             raise kz.KvzipError(s, "paged cache")
 

@@ -65,11 +65,49 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
   return r;
 }
+// four e4m3 codes as two f16x2
+__device__ __forceinline__ void e4m3x4_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 // two floats as e4m3 codes (x in the low byte), round to nearest even
 __device__ __forceinline__ uint32_t pack_e4m3x2(float x, float y) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
   return r;
+}
+
+// (x & mask) | magic in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(magic));
+  return r;
+}
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+// Nibbles 0 and 4 (NIB = 0) or 1 and 5 (NIB = 1) of w as exact f16x2 codes:
+// 0x6400 | c is 1024 + c, 0x6400 | 16 c is 1024 + 16 c.
+template <int NIB>
+__device__ __forceinline__ uint32_t nib_f16x2(uint32_t w) {
+  if constexpr (NIB == 0)
+    return hadd2(and_or(w, 0x000f000fu, 0x64006400u), 0xe400e400u);              // - 1024
+  else
+    return hfma2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd400d400u);   // / 16 - 64
 }
 
 // 16-byte read-only load that is not kept in L1 (each cache byte is used once per CTA)

@@ -64,32 +64,6 @@ __device__ __forceinline__ void mma_fmt(float (&d)[4], uint32_t a0, uint32_t a1,
   else mma_f16(d, a0, a1, a2, a3, b0, b1);
 }
 
-// (x & mask) | magic in one instruction
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t magic) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(mask), "r"(magic));
-  return r;
-}
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-// Nibbles 0 and 4 (NIB = 0) or 1 and 5 (NIB = 1) of w as exact f16x2 codes:
-// 0x6400 | c is 1024 + c, 0x6400 | 16 c is 1024 + 16 c.
-template <int NIB>
-__device__ __forceinline__ uint32_t nib_f16x2(uint32_t w) {
-  if constexpr (NIB == 0)
-    return hadd2(and_or(w, 0x000f000fu, 0x64006400u), 0xe400e400u);              // - 1024
-  else
-    return hfma2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd400d400u);   // / 16 - 64
-}
-
 constexpr int kRowsTile = 64;     // cache rows of a tile: two or four batches, one per warp
 
 template <int FMT, int D>

@@ -465,6 +465,21 @@ __device__ __forceinline__ void tmem_st32_async(uint32_t taddr, const uint32_t (
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16_async(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, "
+      "%9, %10, %11, %12, %13, %14, %15, %16"
+      "};"
+      :
+      : "r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+        "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -474,14 +489,25 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Move a warpgroup's register share (all four warps; N a multiple of 8).
-template <int N>
-__device__ __forceinline__ void regs_grow() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+// Move a warpgroup's registers a thread from the launch's FROM to TO (multiples of
+// 8; all four warps).  Growing waits until other warpgroups have given registers
+// up; the instruction has to name the direction (the wrong one is illegal).  TO = 0: leave
+// them as they are.
+template <int FROM, int TO>
+__device__ __forceinline__ void regs_to() {
+  if constexpr (TO != 0 && TO > FROM)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TO));
+  else if constexpr (TO != 0 && TO < FROM)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TO));
 }
-template <int N>
-__device__ __forceinline__ void regs_shrink() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+
+// One lane of the converged warp, the same in every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // Maxima that return NaN if an operand is NaN.

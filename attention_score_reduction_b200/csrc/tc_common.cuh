@@ -81,6 +81,9 @@ __device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, float (&v)[64]) { t
 __device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, float (&v)[48]) { tmem_ld48(taddr, v); }
 __device__ __forceinline__ void tmem_ld_tile(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
 
+__device__ __forceinline__ void tmem_st_tile(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32_async(taddr, r); }
+__device__ __forceinline__ void tmem_st_tile(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16_async(taddr, r); }
+
 // ------------------------------------------------------------------ host side
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,

@@ -120,6 +120,8 @@ def _ptr(t):
 
 
 def _stream(stream):
+    if isinstance(stream, int):      # a raw cudaStream_t
+        return stream
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
@@ -561,19 +563,26 @@ def cache_struct(fmt: str, k_pages, v_pages, k_params, v_params, page_table, len
                        ptr(v_params), page_table.data_ptr(), lens.data_ptr(), status.data_ptr())
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def cache_write(cache: CacheStruct, k, v, n_rows: int, k_strides, v_strides, starts=None,
                 counts=None, offsets=None, stream=None):
     """kvzip_cache_write; k_strides / v_strides = (unit, row) strides in elements."""
-    _check(_lib.kvzip_cache_write(cache, _ptr(k), _ptr(v), *k_strides, *v_strides, n_rows,
-                                  _ptr(starts), _ptr(counts), _ptr(offsets), _stream(stream)),
-           "kvzip_cache_write")
+    s = _lib.kvzip_cache_write(cache, k.data_ptr(), v.data_ptr(), *k_strides, *v_strides, n_rows,
+                               _addr(starts), _addr(counts), _addr(offsets), _stream(stream))
+    if s:
+        _check(s, "kvzip_cache_write")
 
 
 def cache_read(cache: CacheStruct, k_out, v_out, n_rows: int, starts=None, offsets=None,
                stream=None):
     """kvzip_cache_read"""
-    _check(_lib.kvzip_cache_read(cache, _ptr(k_out), _ptr(v_out), n_rows, _ptr(starts),
-                                 _ptr(offsets), _stream(stream)), "kvzip_cache_read")
+    s = _lib.kvzip_cache_read(cache, k_out.data_ptr(), v_out.data_ptr(), n_rows, _addr(starts),
+                              _addr(offsets), _stream(stream))
+    if s:
+        _check(s, "kvzip_cache_read")
 
 
 def cache_attention_workspace_size(cache: CacheStruct, G: int, n_q: int) -> int:
@@ -583,10 +592,14 @@ def cache_attention_workspace_size(cache: CacheStruct, G: int, n_q: int) -> int:
 def cache_attention(cache: CacheStruct, q, out, workspace, q_lens=None, scale: float = 0.0,
                     stream=None):
     """kvzip_cache_attention; q, out [units][G][n_q][d] (any strides, d contiguous)."""
-    _check(_lib.kvzip_cache_attention(
-        cache, _ptr(q), *q.stride()[:3], _ptr(out), int(out.dtype == torch.float32),
-        *out.stride()[:3], _ptr(q_lens), q.shape[2], q.shape[1], float(scale), _ptr(workspace),
-        workspace.numel(), _stream(stream)), "kvzip_cache_attention")
+    _, G, n_q, _ = q.shape
+    qs, os_ = q.stride(), out.stride()
+    s = _lib.kvzip_cache_attention(
+        cache, q.data_ptr(), qs[0], qs[1], qs[2], out.data_ptr(), out.dtype == torch.float32,
+        os_[0], os_[1], os_[2], _addr(q_lens), n_q, G, scale, workspace.data_ptr(),
+        workspace.numel(), _stream(stream))
+    if s:
+        _check(s, "kvzip_cache_attention")
 
 
 def last_launch_count() -> int:

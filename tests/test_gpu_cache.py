@@ -7,10 +7,11 @@ to bf16 away from the definition.  Attention's tolerance per output element:
     half(out) |out| + (w + 2 (e^delta - 1) + 1e-5) * sum_j p_j |v_j|
 
 half(out) = eps/2 of the output type (the final rounding).  w = the rounding of a
-weight: bf16 on the tensor-memory path (2^-8), fp16 where few query rows read a
-quantised cache (2^-11), two bf16 parts where they read a bf16 cache (2^-16); a
-quantised row on the tensor-memory path is rounded to bf16 as well (2^-8 more in
-v, and in k: a logit error of 2^-8 * reach).  delta bounds the logit: d float32
+weight: fp16 for quantised caches (2^-11); bf16 on the tensor-memory path (2^-8)
+and two bf16 parts where few query rows read the cache (2^-16) otherwise.  On the
+tensor-memory path an int4 row is rounded to fp16 as well (2^-11 more in v, and in
+k: a logit error of 2^-11 * reach), and keys carry one power of two per 64 rows
+(2^-38 of the largest reach).  delta bounds the logit: d float32
 additions of products whose magnitudes add up to `reach`, d * 2^-24 * reach; a
 relative error e^delta - 1 of each weight and of their sum.  1e-5 covers the
 exponentials and the sums over rows.  For int4 the products are with s c and z
@@ -346,7 +347,7 @@ def check_attention(c, q, out, lens, q_lens, scale=None, untouched=None):
     half = torch.finfo(out.dtype).eps / 2
     tc = uses_tensor_memory(G, q.shape[2])
     quant = c.fmt != "bf16"
-    w = 2.0 ** -8 if tc else (2.0 ** -11 if quant else 2.0 ** -16)
+    w = 2.0 ** -11 if quant else (2.0 ** -8 if tc else 2.0 ** -16)
     got = f64(out)
     for u, (n, m) in enumerate(zip(lens, q_lens)):
         k, v = held_values(c, "k", u, n), held_values(c, "v", u, n)
@@ -361,11 +362,12 @@ def check_attention(c, q, out, lens, q_lens, scale=None, untouched=None):
             # weights are the true ones; bound sum p |v| by the largest row instead
             wt = np.broadcast_to(mags[1].max(0) if n else np.zeros(d), wt.shape)
         delta = d * 2.0 ** -24 * reach
+        ww = w
         if tc and quant:
-            delta = delta + 2.0 ** -8 * reach
-            ww = w + 2.0 ** -8
-        else:
-            ww = w
+            delta = delta + 2.0 ** -38 * reach
+        if tc and c.fmt == "int4":
+            delta = delta + 2.0 ** -11 * reach
+            ww = w + 2.0 ** -11
         tol = half * np.abs(want) + (ww + 2 * np.expm1(delta)[..., None] + 1e-5) * wt
         err = np.abs(got[u, :, :m] - want)
         assert np.all(np.isfinite(got[u, :, :m]))
