@@ -5,8 +5,7 @@
 //   out = sum_j softmax_j(scale q.k_j) v_j,  zeros where nothing is seen.
 // With a handful of query rows (decoding: G of them) every cache byte is used
 // once, so the kernel is bound by HBM.  Each warp walks batches of rows of its
-// CTA's piece of the work line with K and V going from global memory straight to
-// the registers of mma.sync fragments, no shared memory in between:
+// CTA's piece of the work line, with mma.sync fragments:
 //   logits  S = Q K^T       M = 16 query rows, N = 8 cache rows, K = 16 elements
 //   output  O^T += V^T P^T  M = 16 elements, N = 8 query rows, K = 16 cache rows
 // The order of the elements inside a product is free as long as both operands
@@ -15,27 +14,34 @@
 // 16 consecutive bytes of four rows (A fragment: `quad` = piece, lane in quad =
 // rows): every load is a whole sector of a row, and pairs of V rows are
 // interleaved with byte permutes.  The accumulator fragment of S is the B
-// fragment of P^T as it stands.  The next batch's K is requested as soon as this
-// batch's logits are formed, the next V as soon as the output is, so that a few
-// KB per warp are always in flight.
+// fragment of P^T as it stands.  Each warp keeps a ring of two or three batches in
+// shared memory that asynchronous copies fill, so that over 100 KB per SM are in
+// flight; batches held in registers (one ahead) reached half of that.
 //
-// Quantised formats multiply the codes themselves, as fp16 (exact for e4m3 and
-// for 0..15), and fold the rows' parameters into logits and weights:
+// Quantised formats multiply the codes themselves, as fp16, and fold the rows'
+// parameters into logits and weights:
 //   x_j = c (s_j S_j + z_j sum(q)),     out = sum_j (p_j s_j) code_j + sum_j p_j z_j.
+// e4m3 codes are exact in fp16.  4-bit codes are not converted at all: masked out of
+// their word, four bits are the fp16 subnormal c 2^-24 (or 16 c 2^-24), which the
+// tensor core multiplies exactly; the powers of two go into Q and the result.
+// Unpacking to fp16 integers instead (two more instructions a pair) left the
+// kernel bound by issue slots.
 // Q goes to fp16 scaled by a power of two per row (a bf16 value is exact in fp16
-// down to 2^-32 of the row's largest).  The weights p_j s_j are formed relative
-// to their own running maximum, as fp16: rounded by at most 2^-11 of a weight,
-// an eighth of the rounding of a bf16 output.  bf16 caches take the weights as
+// down to 2^-28 of the row's largest).  The weights p_j s_j are formed relative
+// to a power of two that follows their largest, as fp16: rounded by at most 2^-11
+// of a weight, an eighth of the rounding of a bf16 output.  bf16 caches take the weights as
 // two bf16 parts (about 16 bits).
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "cache.cuh"
 #include "cache_attention.cuh"
 #include "cache_sched.cuh"
 #include "kvzip_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace kvzip {
 
@@ -64,6 +70,19 @@ __device__ __forceinline__ void mma_fmt(float (&d)[4], uint32_t a0, uint32_t a1,
   else mma_f16(d, a0, a1, a2, a3, b0, b1);
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+
+constexpr float kCodeUnit = 16777216.f;   // 2^24
 constexpr int kRowsTile = 64;     // cache rows of a tile: two or four batches, one per warp
 
 template <int FMT, int D>
@@ -71,22 +90,51 @@ struct RowsCfg {
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int RB = CacheRow<FMT, D>::BYTES;
-  static constexpr int BR = FMT == kFmtBf16 ? 16 : 32;   // cache rows of one batch
+  static constexpr int BR = RB >= 256 ? 16 : 32;         // cache rows of one batch
   static constexpr int NJ = BR / 8;                       // 8-row tiles of the logits
   static constexpr int KC = RB / 64;                      // 16-byte pieces of a K row per lane
   static constexpr int KS = D / 16;                       // k-steps of the logits; m-tiles of the output
+  static constexpr bool QUANT = FMT != kFmtBf16;
+  // a warp's ring of batches: K codes, V codes, K parameters, V parameters
+  static constexpr int SLOTS = RB >= 256 && D == 128 ? 2 : (FMT == kFmtFp8 && D == 128 ? 2 : 3);
+  static constexpr int CODES = BR * RB;
+  static constexpr int SLOT = 2 * CODES + (QUANT ? 8 * BR : 0);
+  static constexpr int RING = WARPS * SLOTS * SLOT;
 };
 
-// Everything a warp carries through its batches of one item.
-template <int FMT, int D, int NT>
-struct RowsState {
-  float m[NT], l[NT], mo[NT], oz[NT];
-  float o[NT][D / 16][4];
-};
+// 16-byte chunk of row r as it lies in shared memory: chunks of a row are exchanged so
+// that neither the K reads (rows quad, chunks of the lane in quad) nor the V reads (rows
+// 2 lane-in-quad, chunks by quad) meet in a bank.
+template <int RB>
+__device__ __forceinline__ int swizzled(int r, int chunk) {
+  if constexpr (RB == 64) return chunk ^ ((r >> 1) & 3);
+  else return chunk ^ ((((r >> 1) & 3) << 1) ^ ((r & 1) << 2));
+}
+
+// Asynchronous copies global -> shared; `bytes` 0 fills with zeros instead.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// CTAs that fit on an SM together, by registers and shared memory.
+constexpr int rows_per_sm(int format, int d, int block) {
+  if (d == 128) return block == 8 ? (format == kFmtInt4 ? 4 : 3) : 2;
+  return format == kFmtBf16 ? 1 : 2;
+}
 
 // NT: 8-row groups of query rows in an item (1 or 2).
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
+__global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 8 * NT))
     cache_attn_rows(const CacheAttnArgs a, const AttnShape shape, int64_t items, float c,
                     float2* __restrict__ ml_out, float* __restrict__ o_out) {
   using Cfg = RowsCfg<FMT, D>;
@@ -94,24 +142,28 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
   constexpr int NJ = Cfg::NJ, KC = Cfg::KC, KS = Cfg::KS, RQ = 8 * NT;
   constexpr bool QUANT = FMT != kFmtBf16;
   __shared__ int64_t scratch[WARPS];
-  __shared__ int64_t found[2];
+  __shared__ LineSpot spot_s;
   __shared__ float xm[WARPS][RQ], xl[WARPS][RQ];
-  __shared__ float xo[WARPS / 2][RQ][D];
+  extern __shared__ __align__(16) uint8_t ring_raw[];
+  // the warps' results, once their rings are read
+  float(*xo)[RQ][D] = reinterpret_cast<float(*)[RQ][D]>(ring_raw);
+  static_assert(WARPS * RQ * D * 4 <= Cfg::RING, "results do not fit where the rings were");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = lane >> 2, qp = lane & 3;
   const int64_t cta = blockIdx.x;
 
   cudaTriggerProgrammaticLaunchCompletion();   // the merge may be launched; it waits for this grid
-  Line<THREADS> line(a.c, shape, items, scratch, found);
+  Line<THREADS> line(a.c, shape, items, scratch, &spot_s);
   const int64_t all = line.all;
   const int64_t n_cta = line_ctas(all, gridDim.x);
   if (cta >= n_cta) return;
   const int64_t p0 = line_cut(all, cta, n_cta), p1 = line_cut(all, cta + 1, n_cta);
-  int64_t w, w_at;
-  line.find(p0, &w, &w_at);
+  const LineSpot spot = line.find(p0);
+  int64_t w = spot.item, w_at = spot.at;
+  AttnItem it = spot.info;
 
   for (int64_t p = p0; p < p1; ++w) {
-    const AttnItem it = attn_item(a.c, shape, w);
+    if (w != spot.item) it = attn_item(a.c, shape, w);
     const int n_tiles = it.n_tiles;
     const int64_t at = w_at;
     w_at += n_tiles;
@@ -121,9 +173,58 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
     p = at + t1;
     const int r_end = min(t1 * kRowsTile, it.vis);
 
+    // ---- batches of this warp: rows r0 + (warp + WARPS n) * BR
+    const int r_first = t0 * kRowsTile + warp * BR;
+    const int lim_all = min(seen_rows(it, it.row0 / shape.G), r_end);   // rows that all queries see
+    const uint32_t ring = smem_u32(ring_raw) + warp * (Cfg::SLOTS * Cfg::SLOT);
+    constexpr int GROUPS = BR / 16;
+    // pool row of each 16-row group of a batch, or -1
+    auto find = [&](int r, int64_t (&base)[GROUPS]) {
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g)
+        base[g] = r + 16 * g < r_end ? cache_slot(a.c, it.u, r + 16 * g) : -1;
+    };
+    // batch of rows r .. into a slot; rows past the end and of a bad page become zeros
+    auto request = [&](int r, uint32_t slot, const int64_t (&base)[GROUPS]) {
+      constexpr int CPR = RB / 16, PER = 32 / CPR > 0 ? 32 / CPR : 1;   // chunks a row, rows a copy
+#pragma unroll
+      for (int i = 0; i < Cfg::CODES / 512; ++i) {
+        const int idx = 32 * i + lane, row = idx / CPR, chunk = idx % CPR;
+        const int g = CPR >= 32 ? (i * 32 / CPR) / 16 : (i * PER) / 16;
+        const int bytes = base[g] >= 0 && r + row < r_end ? 16 : 0;
+        const int64_t at = bytes ? (base[g] + (row & 15)) * RB + 16 * chunk : 0;
+        const uint32_t dst = slot + row * RB + 16 * swizzled<RB>(row, chunk);
+        copy16(dst, static_cast<const uint8_t*>(a.c.k_pages) + at, bytes);
+        copy16(dst + Cfg::CODES, static_cast<const uint8_t*>(a.c.v_pages) + at, bytes);
+      }
+      if constexpr (QUANT) {
+        if (lane < BR) {
+          const int64_t b = BR > 16 && lane >= 16 ? base[GROUPS - 1] : base[0];
+          const int bytes = b >= 0 && r + lane < r_end ? 4 : 0;
+          const int64_t at = bytes ? b + (lane & 15) : 0;
+          copy4(slot + 2 * Cfg::CODES + 4 * lane, a.c.k_params + at, bytes);
+          copy4(slot + 2 * Cfg::CODES + 4 * (BR + lane), a.c.v_params + at, bytes);
+        }
+      }
+    };
+    // the first batches: all their pages, then all their copies, on their way while Q is
+    // prepared
+    {
+      int64_t base[Cfg::SLOTS][GROUPS];
+#pragma unroll
+      for (int n = 0; n < Cfg::SLOTS; ++n) find(r_first + n * WARPS * BR, base[n]);
+#pragma unroll
+      for (int n = 0; n < Cfg::SLOTS; ++n) {
+        if (r_first + n * WARPS * BR < r_end)
+          request(r_first + n * WARPS * BR, ring + n * Cfg::SLOT, base[n]);
+        copies_commit();
+      }
+    }
+
     // ---- query fragments and per-row limits (rows quad and quad + 8 of the item)
     uint32_t qa[KS][2 * NT];
-    float cq[NT], qsum[NT];
+    float cq[NT];        // log2-domain logit = cq S (+ cz z_j for int4)
+    float cz[NT];
     int lim[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -133,265 +234,215 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
       lim[t] = live ? seen_rows(it, tok) : 0;
       const uint16_t* qr = static_cast<const uint16_t*>(a.q) + it.u * a.q_unit +
                            (row - tok * shape.G) * a.q_head + tok * a.q_row;
-      float f = 1.f;
-      if constexpr (QUANT) {
-        // the row's largest magnitude, then a power of two that lifts it to [2^14, 2^15)
-        uint32_t top = 0;
-        if (live) {
-          const uint4* q4 = reinterpret_cast<const uint4*>(qr) + qp * (D / 32);
+      // the pairs of fragment columns 2 qp and 2 qp + 8 of every k-step, as bf16
+      uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint4 v = q4[i];
-            const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              top = max(top, max((ws[k] << 16) & 0x7fff0000u, ws[k] & 0x7fff0000u));
-          }
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if constexpr (FMT == kFmtInt4) {
+          // a word of codes: elements e0..e7 -> (e0, e4), (e1, e5) then (e2, e6), (e3, e7)
+          if (live) v = *reinterpret_cast<const uint4*>(qr + 128 * (ks / 8) + 32 * qp + 4 * (ks % 8));
+          v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                         __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+        } else {
+          const int el = FMT == kFmtBf16 ? 32 * (ks / 2) + 8 * qp : 64 * (ks / 4) + 16 * qp + 4 * (ks & 3);
+          if (live) v = *reinterpret_cast<const uint4*>(qr + el);
         }
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          qa[ks + k / 2][2 * t + (k & 1)] = w[k];
+          if constexpr (QUANT) top = max(top, max((w[k] << 16) & 0x7fff0000u, w[k] & 0x7fff0000u));
+        }
+      }
+      cq[t] = c;
+      cz[t] = 0.f;
+      if constexpr (QUANT) {
+        // fp16, the row's largest element lifted to [2^14, 2^15)
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = static_cast<int>(top >> 23) - 127;       // -127 for zeros and subnormals
-        f = __uint_as_float(static_cast<uint32_t>(min(max(127 + 14 - e, 1), 254)) << 23);
-      }
-      cq[t] = QUANT ? c / f : c;
-      float sum = 0.f;
+        const float f = __uint_as_float(static_cast<uint32_t>(min(max(127 + 14 - e, 1), 254)) << 23);
+        // int4: codes meet Q as fp16 subnormals c 2^-24, those of the odd pairs as 16 c 2^-24
+        const float f1 = FMT == kFmtInt4 ? f * 0.0625f : f;
+        float sum = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint32_t w0 = 0, w1 = 0;      // the pairs of fragment columns 2 qp and 2 qp + 8
-        if (live) {
-          if constexpr (FMT == kFmtInt4) {
-            // word ks / 2 of the lane's pieces: elements e0..e7; (e0, e4), (e1, e5) then (e2, e6), (e3, e7)
-            const int el = 128 * (ks / 8) + 32 * qp + 8 * ((ks % 8) / 2) + 2 * (ks & 1);
-            w0 = qr[el] | (static_cast<uint32_t>(qr[el + 4]) << 16);
-            w1 = qr[el + 1] | (static_cast<uint32_t>(qr[el + 5]) << 16);
-          } else {
-            const int el = FMT == kFmtBf16 ? 32 * (ks / 2) + 8 * qp + 4 * (ks & 1)
-                                           : 64 * (ks / 4) + 16 * qp + 4 * (ks & 3);
-            const uint2 v = *reinterpret_cast<const uint2*>(qr + el);
-            w0 = v.x;
-            w1 = v.y;
-          }
-          if constexpr (QUANT) {
-            const float f0 = bf16_lo(w0) * f, f1 = bf16_hi(w0) * f;
-            const float f2 = bf16_lo(w1) * f, f3 = bf16_hi(w1) * f;
-            sum += (f0 + f1) + (f2 + f3);
-            w0 = pack_f16x2(f0, f1);
-            w1 = pack_f16x2(f2, f3);
-          }
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint32_t w0 = qa[ks][2 * t], w1 = qa[ks][2 * t + 1];
+          sum += (bf16_lo(w0) + bf16_hi(w0)) + (bf16_lo(w1) + bf16_hi(w1));
+          qa[ks][2 * t] = pack_f16x2(bf16_lo(w0) * f, bf16_hi(w0) * f);
+          qa[ks][2 * t + 1] = pack_f16x2(bf16_lo(w1) * f1, bf16_hi(w1) * f1);
         }
-        qa[ks][2 * t] = w0;
-        qa[ks][2 * t + 1] = w1;
+        cq[t] = c / f;
+        if constexpr (FMT == kFmtInt4) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          cq[t] *= kCodeUnit;
+          cz[t] = c * sum;
+        }
       }
-      if constexpr (FMT == kFmtInt4) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      }
-      qsum[t] = sum;
     }
 
-    RowsState<FMT, D, NT> st;
+    // State of the query rows this lane has in the logits: running maximum m and sum l
+    // (this lane's columns); quantised: weights p s are formed as fp16 relative to a
+    // power of two, a = p s F, with the largest so far, top_a, kept within 2^-2 .. 2^12;
+    // int4: oz = sum p z.
+    float m[NT], l[NT], F[NT], top_a[NT], oz[NT];
+    float o[NT][KS][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      st.m[t] = st.mo[t] = -INFINITY;
-      st.l[t] = st.oz[t] = 0.f;
+      m[t] = -INFINITY;
+      l[t] = oz[t] = top_a[t] = 0.f;
+      F[t] = 1.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) st.o[t][k][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[t][k][e] = 0.f;
     }
 
-    // ---- batches of this warp: rows r0 + (warp + WARPS n) * BR
-    const int r_first = t0 * kRowsTile + warp * BR;
-    int64_t base[BR / 16];               // pool row of each 16-row group of the batch, or -1
-    auto find = [&](int r) {
-#pragma unroll
-      for (int g = 0; g < BR / 16; ++g)
-        base[g] = r + 16 * g < r_end ? cache_slot(a.c, it.u, r + 16 * g) : -1;
-    };
-    uint4 kreg[NJ][KC];
-    uint4 vreg[BR / 4][RB / 128 > 0 ? RB / 128 : 1];
-    uint2 kpar[QUANT ? NJ : 1], vpar[QUANT ? NJ : 1];
-    const uint8_t* kp = static_cast<const uint8_t*>(a.c.k_pages);
-    const uint8_t* vp = static_cast<const uint8_t*>(a.c.v_pages);
-    auto load_k = [&](int r) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int64_t b = base[j / 2];
-        const bool ok = b >= 0 && r + 8 * j + quad < r_end;
-        const uint8_t* src = kp + (b + 8 * (j & 1) + quad) * RB + 16 * qp;
-#pragma unroll
-        for (int k = 0; k < KC; ++k)
-          kreg[j][k] = ok ? ldg_stream16(src + 64 * k) : make_uint4(0, 0, 0, 0);
-        if constexpr (QUANT) {
-          const int64_t pr = b + 8 * (j & 1) + 2 * qp;
-          kpar[j] = b >= 0 ? ldg_stream8(a.c.k_params + pr) : make_uint2(0, 0);
-        }
-      }
-    };
-    // rows of this lane's V registers: group g = 16 g + {0, 1, 8, 9} + 2 qp
-    auto load_v = [&](int r) {
-#pragma unroll
-      for (int g = 0; g < BR / 16; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int dr = 2 * qp + (i & 1) + 8 * (i >> 1);
-          const bool ok = base[g] >= 0 && r + 16 * g + dr < r_end;
-          const uint8_t* src = vp + (base[g] + dr) * RB;
-          if constexpr (RB >= 128) {
-#pragma unroll
-            for (int h = 0; h < RB / 128; ++h)
-              vreg[4 * g + i][h] =
-                  ok ? ldg_stream16(src + 128 * h + 16 * quad) : make_uint4(0, 0, 0, 0);
-          } else {
-            const uint2 v = ok ? ldg_stream8(src + 8 * quad) : make_uint2(0, 0);
-            vreg[4 * g + i][0].x = v.x;
-            vreg[4 * g + i][0].y = v.y;
-          }
-        }
-      if constexpr (QUANT) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const int64_t pr = base[j / 2] + 8 * (j & 1) + 2 * qp;
-          vpar[j] = base[j / 2] >= 0 ? ldg_stream8(a.c.v_params + pr) : make_uint2(0, 0);
-        }
-      }
-    };
-    if (r_first < r_end) {
-      find(r_first);
-      load_k(r_first);
-      load_v(r_first);
-    }
+    int n_slot = 0;
     for (int r = r_first; r < r_end; r += WARPS * BR) {
-      const int rn = r + WARPS * BR;
-      // ---- logits
+      const int rn = r + Cfg::SLOTS * WARPS * BR;          // the batch that takes this one's slot
+      int64_t base[GROUPS];
+      find(rn, base);
+      const uint32_t slot = ring + n_slot * Cfg::SLOT;
+      n_slot = n_slot + 1 == Cfg::SLOTS ? 0 : n_slot + 1;
+      copies_wait<Cfg::SLOTS - 1>();
+      __syncwarp();
+      // ---- products of the logits
       float s[NJ][4];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+        auto qk = [&](int ks, uint32_t b0, uint32_t b1) {
+          mma_fmt<FMT>(s[j], qa[ks][0], NT > 1 ? qa[ks][2 * NT - 2] : 0u, qa[ks][1],
+                       NT > 1 ? qa[ks][2 * NT - 1] : 0u, b0, b1);
+        };
 #pragma unroll
         for (int k = 0; k < KC; ++k) {
-          const uint32_t ws[4] = {kreg[j][k].x, kreg[j][k].y, kreg[j][k].z, kreg[j][k].w};
+          const int row = 8 * j + quad;
+          const uint4 kw = lds16(slot + row * RB + 16 * swizzled<RB>(row, 4 * k + qp));
+          const uint32_t ws[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             if constexpr (FMT == kFmtBf16) {
               if (i & 1) continue;
-              const int ks = 2 * k + i / 2;
-              mma_bf16(s[j], qa[ks][0], NT > 1 ? qa[ks][2 * NT - 2] : 0u, qa[ks][1],
-                       NT > 1 ? qa[ks][2 * NT - 1] : 0u, ws[i], ws[i + 1]);
+              qk(2 * k + i / 2, ws[i], ws[i + 1]);
             } else if constexpr (FMT == kFmtFp8) {
-              const int ks = 4 * k + i;
-              mma_f16(s[j], qa[ks][0], NT > 1 ? qa[ks][2 * NT - 2] : 0u, qa[ks][1],
-                      NT > 1 ? qa[ks][2 * NT - 1] : 0u, e4m3x2_f16x2(ws[i]),
-                      e4m3x2_f16x2(ws[i] >> 16));
+              uint32_t lo, hi;
+              e4m3x4_f16x2(ws[i], lo, hi);
+              qk(4 * k + i, lo, hi);
             } else {
-              const int ks = 8 * k + 2 * i;
-              mma_f16(s[j], qa[ks][0], NT > 1 ? qa[ks][2 * NT - 2] : 0u, qa[ks][1],
-                      NT > 1 ? qa[ks][2 * NT - 1] : 0u, nib_f16x2<0>(ws[i]), nib_f16x2<1>(ws[i]));
-              mma_f16(s[j], qa[ks + 1][0], NT > 1 ? qa[ks + 1][2 * NT - 2] : 0u, qa[ks + 1][1],
-                      NT > 1 ? qa[ks + 1][2 * NT - 1] : 0u, nib_f16x2<0>(ws[i] >> 8),
-                      nib_f16x2<1>(ws[i] >> 8));
+              qk(8 * k + 2 * i, ws[i] & 0x000f000fu, ws[i] & 0x00f000f0u);
+              qk(8 * k + 2 * i + 1, (ws[i] >> 8) & 0x000f000fu, (ws[i] >> 8) & 0x00f000f0u);
             }
           }
         }
       }
-      uint2 kpar_now[QUANT ? NJ : 1];
+      uint2 kpar[QUANT ? NJ : 1], vpar[QUANT ? NJ : 1];     // rows 8 j + 2 qp, + 1
       if constexpr (QUANT) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) kpar_now[j] = kpar[j];
+        for (int j = 0; j < NJ; ++j) {
+          kpar[j] = lds8(slot + 2 * Cfg::CODES + 4 * (8 * j + 2 * qp));
+          vpar[j] = lds8(slot + 2 * Cfg::CODES + 4 * (BR + 8 * j + 2 * qp));
+        }
       }
-      // ---- request the next batch's K (its pages first); this batch's V is on its way
-      if (rn < r_end) {
-        find(rn);
-        load_k(rn);
-      }
-      // ---- scaled logits (log2 domain), masked
-      float alpha_o[NT];
+      // ---- logits (log2 domain) in place, their maximum, weights
+      float scale_o[NT];
       uint32_t phi[NT][NJ], plo[NT][QUANT ? 1 : NJ];
       bool moved = false;
+      auto softmax = [&](auto mask_tag) {
+        constexpr bool MASK = decltype(mask_tag)::value;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        float x[NJ][2];
-        float mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = s[j][2 * t + e];
-            if constexpr (FMT == kFmtFp8) {
-              v *= __uint_as_float(e ? kpar_now[j].y : kpar_now[j].x);
-            } else if constexpr (FMT == kFmtInt4) {
-              const uint32_t par = e ? kpar_now[j].y : kpar_now[j].x;
-              v = fmaf(v, bf16_lo(par), bf16_hi(par) * qsum[t]);
-            }
-            x[j][e] = r + 8 * j + 2 * qp + e < lim[t] ? v * cq[t] : -INFINITY;
-            mx = fmaxf(mx, x[j][e]);
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(st.m[t], mx);
-        const float m_sub = m_new == -INFINITY ? 0.f : m_new;   // nothing seen yet
-        const float alpha = exp2f(st.m[t] - m_sub);
-        moved |= m_new != st.m[t];
-        st.m[t] = m_new;
-        float sum = 0.f;
-        if constexpr (!QUANT) {
-#pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const float e0 = exp2f(x[j][0] - m_sub), e1 = exp2f(x[j][1] - m_sub);
-            sum += e0 + e1;
-            phi[t][j] = pack_bf16x2(e0, e1);
-            plo[t][j] = pack_bf16x2(e0 - bf16_lo(phi[t][j]), e1 - bf16_hi(phi[t][j]));
-          }
-          alpha_o[t] = alpha;
-        } else {
-          // weights p s relative to their own maximum: y = x + log2 s
-          float y[NJ][2], my = -INFINITY, z = 0.f;
+        for (int t = 0; t < NT; ++t) {
+          float mx = -INFINITY;
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint32_t par = e ? vpar[j].y : vpar[j].x;
-              const float pe = exp2f(x[j][e] - m_sub);
-              sum += pe;
-              float ls;
-              if constexpr (FMT == kFmtFp8) {
-                // the exponent of 2^e; a NaN scale (a row with a non-finite element) stays NaN
-                ls = par < 0x7f800000u ? static_cast<float>(static_cast<int>(par >> 23) - 127)
-                                       : __uint_as_float(0x7fc00000u);
-              } else {
-                ls = __log2f(bf16_lo(par));
-                // a masked row's zero may be anything: only seen rows count
-                z += r + 8 * j + 2 * qp + e < lim[t] ? pe * bf16_hi(par) : 0.f;
-              }
-              y[j][e] = r + 8 * j + 2 * qp + e < lim[t] ? x[j][e] + ls : -INFINITY;
-              my = fmaxf(my, y[j][e]);
+              float& x = s[j][2 * t + e];
+              const uint32_t par = QUANT ? (e ? kpar[j].y : kpar[j].x) : 0u;
+              if constexpr (FMT == kFmtFp8) x *= __uint_as_float(par) * cq[t];
+              else if constexpr (FMT == kFmtInt4) x = fmaf(x, bf16_lo(par) * cq[t], bf16_hi(par) * cz[t]);
+              else x *= cq[t];
+              if (MASK) x = r + 8 * j + 2 * qp + e < lim[t] ? x : -INFINITY;
+              mx = fmaxf(mx, x);
             }
-          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 1));
-          my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 2));
-          const float mo_new = fmaxf(st.mo[t], my);
-          const float mo_sub = mo_new == -INFINITY ? 0.f : mo_new;
-          alpha_o[t] = exp2f(st.mo[t] - mo_sub);
-          moved |= mo_new != st.mo[t];
-          st.mo[t] = mo_new;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float m_new = fmaxf(m[t], mx);
+          const float m_sub = m_new == -INFINITY ? 0.f : m_new;   // nothing seen yet
+          const float alpha = ex2_approx(m[t] - m_sub);
+          moved |= m_new != m[t];
+          m[t] = m_new;
+          float sum = 0.f;
 #pragma unroll
           for (int j = 0; j < NJ; ++j)
-            phi[t][j] = pack_f16x2(exp2f(y[j][0] - mo_sub), exp2f(y[j][1] - mo_sub));
-          st.oz[t] = st.oz[t] * alpha + z;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float& x = s[j][2 * t + e];
+              x = ex2_approx(x - m_sub);
+              sum += x;
+            }
+          l[t] = fmaf(l[t], alpha, sum);
+          scale_o[t] = alpha;
+          if constexpr (!QUANT) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const float e0 = s[j][2 * t], e1 = s[j][2 * t + 1];
+              phi[t][j] = pack_bf16x2(e0, e1);
+              plo[t][j] = pack_bf16x2(e0 - bf16_lo(phi[t][j]), e1 - bf16_hi(phi[t][j]));
+            }
+          } else {
+            float z = 0.f, ta = 0.f;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float& x = s[j][2 * t + e];
+                uint32_t par = e ? vpar[j].y : vpar[j].x;
+                // a row that this query does not see may hold anything
+                if (MASK) par = r + 8 * j + 2 * qp + e < lim[t] ? par : 0u;
+                if constexpr (FMT == kFmtFp8) {
+                  x *= __uint_as_float(par);
+                } else {
+                  z = fmaf(x, bf16_hi(par), z);
+                  x *= bf16_lo(par);
+                }
+                ta = fmaxf(ta, x);
+              }
+            oz[t] = fmaf(oz[t], alpha, z);
+            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 1));
+            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 2));
+            top_a[t] = fmaxf(top_a[t] * alpha, ta);
+            const float lead = top_a[t] * F[t];
+            if (top_a[t] > 0.f && !(lead <= 4096.f && lead >= 0.25f)) {
+              const int e = static_cast<int>(__float_as_uint(top_a[t]) >> 23);
+              const float f = __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 253)) << 23);
+              scale_o[t] *= f / F[t];
+              F[t] = f;
+              moved = true;
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+              phi[t][j] = pack_f16x2(s[j][2 * t] * F[t], s[j][2 * t + 1] * F[t]);
+          }
         }
-        st.l[t] = st.l[t] * alpha + sum;
-      }
+      };
+      if (r + BR > lim_all) softmax(std::true_type{});
+      else softmax(std::false_type{});
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const float a_lo = __shfl_sync(0xffffffffu, alpha_o[t], 8 * qp);
-          const float a_hi = __shfl_sync(0xffffffffu, alpha_o[t], 8 * qp + 4);
+          const float a_lo = __shfl_sync(0xffffffffu, scale_o[t], 8 * qp);
+          const float a_hi = __shfl_sync(0xffffffffu, scale_o[t], 8 * qp + 4);
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
-            st.o[t][k][0] *= a_lo;
-            st.o[t][k][1] *= a_hi;
-            st.o[t][k][2] *= a_lo;
-            st.o[t][k][3] *= a_hi;
+            o[t][k][0] *= a_lo;
+            o[t][k][1] *= a_hi;
+            o[t][k][2] *= a_lo;
+            o[t][k][3] *= a_hi;
           }
         }
       }
@@ -401,64 +452,86 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
         auto pv = [&](int mt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            mma_fmt<FMT>(st.o[t][mt], a0, a1, a2, a3, phi[t][2 * g], phi[t][2 * g + 1]);
-            if constexpr (!QUANT)
-              mma_bf16(st.o[t][mt], a0, a1, a2, a3, plo[t][2 * g], plo[t][2 * g + 1]);
+            mma_fmt<FMT>(o[t][mt], a0, a1, a2, a3, phi[t][2 * g], phi[t][2 * g + 1]);
+            if constexpr (!QUANT) mma_bf16(o[t][mt], a0, a1, a2, a3, plo[t][2 * g], plo[t][2 * g + 1]);
           }
         };
-        constexpr int WORDS = RB / 32;      // 32-bit words of a V row per lane
+        uint32_t vw[4][4];
+        // this lane's 16 (RB = 64: 8) bytes of rows 16 g + {0, 1, 8, 9} + 2 qp
+        constexpr int VW = RB >= 128 ? 4 : 2;         // 32-bit words of one piece
 #pragma unroll
-        for (int wd = 0; wd < WORDS; ++wd) {
-          uint32_t v[4];
+        for (int wd = 0; wd < RB / 32; ++wd) {
+          if (wd % VW == 0) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4& q4 = vreg[4 * g + i][wd / 4];
-            v[i] = wd % 4 == 0 ? q4.x : (wd % 4 == 1 ? q4.y : (wd % 4 == 2 ? q4.z : q4.w));
+            for (int i = 0; i < 4; ++i) {
+              const int row = 16 * g + 2 * qp + (i & 1) + 8 * (i >> 1);
+              const uint32_t at = slot + Cfg::CODES + row * RB;
+              if constexpr (RB >= 128) {
+                const uint4 q4 = lds16(at + 16 * swizzled<RB>(row, 8 * (wd / 4) + quad));
+                vw[i][0] = q4.x;
+                vw[i][1] = q4.y;
+                vw[i][2] = q4.z;
+                vw[i][3] = q4.w;
+              } else {
+                const uint2 q2 = lds8(at + 16 * swizzled<RB>(row, quad >> 1) + 8 * (quad & 1));
+                vw[i][0] = q2.x;
+                vw[i][1] = q2.y;
+              }
+            }
           }
+          const uint32_t v[4] = {vw[0][wd % VW], vw[1][wd % VW], vw[2][wd % VW], vw[3][wd % VW]};
           if constexpr (FMT == kFmtBf16) {
             pv(wd, __byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632),
                __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[2], v[3], 0x7632));
           } else if constexpr (FMT == kFmtFp8) {
-            const uint32_t x0 = __byte_perm(v[0], v[1], 0x5140), x1 = __byte_perm(v[0], v[1], 0x7362);
-            const uint32_t y0 = __byte_perm(v[2], v[3], 0x5140), y1 = __byte_perm(v[2], v[3], 0x7362);
-            pv(2 * wd, e4m3x2_f16x2(x0), e4m3x2_f16x2(x0 >> 16), e4m3x2_f16x2(y0),
-               e4m3x2_f16x2(y0 >> 16));
-            pv(2 * wd + 1, e4m3x2_f16x2(x1), e4m3x2_f16x2(x1 >> 16), e4m3x2_f16x2(y1),
-               e4m3x2_f16x2(y1 >> 16));
+            uint32_t x0, x1, x2, x3, y0, y1, y2, y3;
+            e4m3x4_f16x2(__byte_perm(v[0], v[1], 0x5140), x0, x1);
+            e4m3x4_f16x2(__byte_perm(v[0], v[1], 0x7362), x2, x3);
+            e4m3x4_f16x2(__byte_perm(v[2], v[3], 0x5140), y0, y1);
+            e4m3x4_f16x2(__byte_perm(v[2], v[3], 0x7362), y2, y3);
+            pv(2 * wd, x0, x1, y0, y1);
+            pv(2 * wd + 1, x2, x3, y2, y3);
           } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t x = __byte_perm(v[0], v[1], h ? 0x7632 : 0x5410);
               const uint32_t y = __byte_perm(v[2], v[3], h ? 0x7632 : 0x5410);
-              pv(4 * wd + 2 * h, nib_f16x2<0>(x), nib_f16x2<1>(x), nib_f16x2<0>(y), nib_f16x2<1>(y));
-              pv(4 * wd + 2 * h + 1, nib_f16x2<0>(x >> 8), nib_f16x2<1>(x >> 8),
-                 nib_f16x2<0>(y >> 8), nib_f16x2<1>(y >> 8));
+              pv(4 * wd + 2 * h, x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u);
+              pv(4 * wd + 2 * h + 1, (x >> 8) & 0x000f000fu, (x >> 8) & 0x00f000f0u,
+                 (y >> 8) & 0x000f000fu, (y >> 8) & 0x00f000f0u);
             }
           }
         }
       }
-      if (rn < r_end) load_v(rn);
+      __syncwarp();                      // the slot is read
+      if (rn < r_end) request(rn, slot, base);
+      copies_commit();
     }
+    copies_wait<0>();
+    __syncthreads();                     // every warp's ring is read: results go there
 
     // ---- this warp's result, relative to 2^m: o = sum p v
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      st.l[t] += __shfl_xor_sync(0xffffffffu, st.l[t], 1);
-      st.l[t] += __shfl_xor_sync(0xffffffffu, st.l[t], 2);
+      l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
+      l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
       if constexpr (QUANT) {
-        st.oz[t] += __shfl_xor_sync(0xffffffffu, st.oz[t], 1);
-        st.oz[t] += __shfl_xor_sync(0xffffffffu, st.oz[t], 2);
-        const float f = st.mo[t] == -INFINITY ? 0.f : exp2f(st.mo[t] - st.m[t]);
+        oz[t] += __shfl_xor_sync(0xffffffffu, oz[t], 1);
+        oz[t] += __shfl_xor_sync(0xffffffffu, oz[t], 2);
+        const float f = 1.f / F[t];
         const float f0 = __shfl_sync(0xffffffffu, f, 8 * qp);
         const float f1 = __shfl_sync(0xffffffffu, f, 8 * qp + 4);
-        const float z0 = __shfl_sync(0xffffffffu, st.oz[t], 8 * qp);
-        const float z1 = __shfl_sync(0xffffffffu, st.oz[t], 8 * qp + 4);
+        const float z0 = __shfl_sync(0xffffffffu, oz[t], 8 * qp);
+        const float z1 = __shfl_sync(0xffffffffu, oz[t], 8 * qp + 4);
+        // int4: codes were c 2^-24, and 16 c 2^-24 in the fragment's second row
+        constexpr float u0 = FMT == kFmtInt4 ? kCodeUnit : 1.f;
+        constexpr float u1 = FMT == kFmtInt4 ? kCodeUnit / 16.f : 1.f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          st.o[t][k][0] = fmaf(st.o[t][k][0], f0, z0);
-          st.o[t][k][1] = fmaf(st.o[t][k][1], f1, z1);
-          st.o[t][k][2] = fmaf(st.o[t][k][2], f0, z0);
-          st.o[t][k][3] = fmaf(st.o[t][k][3], f1, z1);
+          o[t][k][0] = fmaf(o[t][k][0] * u0, f0, z0);
+          o[t][k][1] = fmaf(o[t][k][1] * u0, f1, z1);
+          o[t][k][2] = fmaf(o[t][k][2] * u1, f0, z0);
+          o[t][k][3] = fmaf(o[t][k][3] * u1, f1, z1);
         }
       }
     }
@@ -471,75 +544,57 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS)
       else
         return (D / 8) * quad + 2 * mt + (e >> 1);
     };
-    // ---- merge the warps pairwise: the upper half hands over, the lower half adds
-    for (int half = WARPS / 2; half >= 1; half >>= 1) {
-      if (warp >= half && warp < 2 * half) {
+    // ---- join the warps: everything through shared memory, eight elements a thread
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (qp == 0) {
-            xm[warp][quad + 8 * t] = st.m[t];
-            xl[warp][quad + 8 * t] = st.l[t];
-          }
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              xo[warp - half][2 * qp + (e & 1) + 8 * t][elem(k, e)] = st.o[t][k][e];
-        }
+    for (int t = 0; t < NT; ++t) {
+      if (qp == 0) {
+        xm[warp][quad + 8 * t] = m[t];
+        xl[warp][quad + 8 * t] = l[t];
       }
-      __syncthreads();
-      if (warp < half) {
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float m2 = xm[warp + half][quad + 8 * t], l2 = xl[warp + half][quad + 8 * t];
-          const float M = fmaxf(st.m[t], m2);
-          const float sub = M == -INFINITY ? 0.f : M;
-          const float fa = exp2f(st.m[t] - sub), fb = exp2f(m2 - sub);
-          st.m[t] = M;
-          st.l[t] = st.l[t] * fa + l2 * fb;
-          const float a0 = __shfl_sync(0xffffffffu, fa, 8 * qp), a1 = __shfl_sync(0xffffffffu, fa, 8 * qp + 4);
-          const float b0 = __shfl_sync(0xffffffffu, fb, 8 * qp), b1 = __shfl_sync(0xffffffffu, fb, 8 * qp + 4);
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-          for (int k = 0; k < KS; ++k)
+        for (int e = 0; e < 4; e += 2)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              st.o[t][k][e] = st.o[t][k][e] * ((e & 1) ? a1 : a0) +
-                              xo[warp][2 * qp + (e & 1) + 8 * t][elem(k, e)] * ((e & 1) ? b1 : b0);
-        }
-      }
-      __syncthreads();
-    }
-    // ---- warp 0 holds the CTA's result; it goes out through shared memory in row order
-    if (warp == 0) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (qp == 0) {
-          xm[0][quad + 8 * t] = st.m[t];
-          xl[0][quad + 8 * t] = st.l[t];
-        }
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            xo[0][2 * qp + (e & 1) + 8 * t][elem(k, e)] = st.o[t][k][e];
-      }
+          for (int b = 0; b < 2; ++b)
+            xo[warp][2 * qp + b + 8 * t][elem(k, e)] = o[t][k][e + b];
     }
     __syncthreads();
-    if (t0 == 0 && t1 == n_tiles) {
-      for (int i = threadIdx.x; i < it.rows * (D / 8); i += THREADS) {
-        const int row = i / (D / 8), e = (i % (D / 8)) * 8;
-        const float inv = xl[0][row] > 0.f ? 1.f / xl[0][row] : (xl[0][row] == 0.f ? 0.f : NAN);
-        float v[8];
+    const bool whole = t0 == 0 && t1 == n_tiles;
+    const int64_t slot = line_slot(all, cta, n_cta, at);
+    for (int i = threadIdx.x; i < it.rows * (D / 8); i += THREADS) {
+      const int row = i / (D / 8), e = (i % (D / 8)) * 8;
+      float M = xm[0][row];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = xo[0][row][e + k] * inv;
-        attn_store8(a, shape, it, row, e, v);
+      for (int k = 1; k < WARPS; ++k) M = fmaxf(M, xm[k][row]);
+      const float sub = M == -INFINITY ? 0.f : M;
+      float L = 0.f, v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        const float f = ex2_approx(xm[k][row] - sub);
+        L = fmaf(xl[k][row], f, L);
+        const float4 x = *reinterpret_cast<const float4*>(&xo[k][row][e]);
+        const float4 y = *reinterpret_cast<const float4*>(&xo[k][row][e + 4]);
+        v[0] = fmaf(x.x, f, v[0]);
+        v[1] = fmaf(x.y, f, v[1]);
+        v[2] = fmaf(x.z, f, v[2]);
+        v[3] = fmaf(x.w, f, v[3]);
+        v[4] = fmaf(y.x, f, v[4]);
+        v[5] = fmaf(y.y, f, v[5]);
+        v[6] = fmaf(y.z, f, v[6]);
+        v[7] = fmaf(y.w, f, v[7]);
       }
-    } else {
-      const int64_t slot = line_slot(all, cta, n_cta, at);
-      for (int i = threadIdx.x; i < RQ * D / 4; i += THREADS)
-        reinterpret_cast<float4*>(o_out + slot * RQ * D)[i] =
-            reinterpret_cast<const float4*>(&xo[0][0][0])[i];
-      if (threadIdx.x < RQ) ml_out[slot * RQ + threadIdx.x] = make_float2(xm[0][threadIdx.x], xl[0][threadIdx.x]);
+      if (whole) {
+        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] *= inv;
+        attn_store8(a, shape, it, row, e, v);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(o_out + (slot * RQ + row) * D + e);
+        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        if (e == 0) ml_out[slot * RQ + row] = make_float2(M, L);
+      }
     }
     __syncthreads();
   }
@@ -550,13 +605,16 @@ cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st, int* launches) 
   using Cfg = RowsCfg<FMT, D>;
   const AttnShape shape = attn_shape(a.q_lens, a.n_q, a.G, 8 * NT, kRowsTile);
   const int64_t items = a.c.units * shape.blocks;
-  const int ctas = rows_ctas(a.c.format, D);
+  const int ctas = rows_ctas(FMT, D, shape.block);
   float2* ml = static_cast<float2*>(a.ws);
   float* o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) +
                                       attn_ml_bytes(ctas, shape.block));
-  cache_attn_rows<FMT, D, NT><<<ctas, Cfg::THREADS, 0, st>>>(
+  cudaError_t e = cudaFuncSetAttribute(cache_attn_rows<FMT, D, NT>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::RING);
+  if (e != cudaSuccess) return e;
+  cache_attn_rows<FMT, D, NT><<<ctas, Cfg::THREADS, Cfg::RING, st>>>(
       a, shape, items, a.scale * 1.4426950408889634f, ml, o);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   *launches += 2;
   return launch_attn_merge(a, shape, items, ctas, ml, o, st);
@@ -564,9 +622,8 @@ cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st, int* launches) 
 
 }  // namespace
 
-// CTAs of the work line: as many as fit on the 148 SMs together (their registers
-// allow three per SM, two for bf16 rows of 256).
-int rows_ctas(int format, int d) { return 148 * (format == kFmtBf16 && d == 256 ? 2 : 3); }
+// CTAs of the work line: all resident on the 148 SMs at once.
+int rows_ctas(int format, int d, int block) { return 148 * rows_per_sm(format, d, block); }
 
 int rows_block(int64_t rows) { return rows <= 8 ? 8 : 16; }
 

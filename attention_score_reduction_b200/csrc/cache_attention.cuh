@@ -46,7 +46,7 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
                               int ctas, const float2* ml, const float* o, cudaStream_t st);
 
 // Few query rows a unit: mma.sync, straight from global memory.
-int rows_ctas(int format, int d);
+int rows_ctas(int format, int d, int block);
 int rows_block(int64_t rows);      // query rows of an item, for `rows` rows a unit
 cudaError_t launch_cache_attn_rows(const CacheAttnArgs& a, cudaStream_t s, int* launches);
 

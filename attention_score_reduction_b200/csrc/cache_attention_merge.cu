@@ -68,29 +68,29 @@ __global__ void __launch_bounds__(kMergeThreads)
     cache_attn_merge(const CacheAttnArgs a, const AttnShape shape, int64_t items, int ctas,
                      int by_item, const float2* __restrict__ ml, const float* __restrict__ o) {
   __shared__ int64_t scratch[kMergeWarps];
-  __shared__ int64_t found[2];
+  __shared__ LineSpot spot_s;
   __shared__ RowPart<D> acc_s[kMergeWarps][32];
   __shared__ float l_s[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int64_t w = blockIdx.x, before = 0;
   bool split = false;
   int64_t c0 = 0, c1 = 0;                // CTAs with a part of the item, inclusive
-  Line<kMergeThreads> t(a.c, shape, items, scratch, found);
+  Line<kMergeThreads> t(a.c, shape, items, scratch, &spot_s);
   const int64_t n = line_ctas(t.all, ctas);
+  LineSpot spot;
   if (by_item) {
-    before = t.before(w);
-  } else if (w + 1 < n) {
-    const int64_t cut = line_cut(t.all, w + 1, n);
-    const int64_t last = line_cut(t.all, w, n);
-    t.find(cut, &w, &before);
-    split = before < cut && last <= before;          // the first cut inside item w
+    spot = t.of_item(blockIdx.x);
+    split = spot.info.n_tiles > 0;
+  } else if (blockIdx.x + 1 < n) {
+    const int64_t cut = line_cut(t.all, blockIdx.x + 1, n);
+    spot = t.find(cut);
+    // the first cut inside the item
+    split = spot.at < cut && line_cut(t.all, blockIdx.x, n) <= spot.at;
   }
-  const AttnItem it = attn_item(a.c, shape, by_item || split ? w : 0);
-  if (by_item || split) {
-    if (it.n_tiles > 0) {
-      c0 = line_cta(t.all, before, n);
-      c1 = line_cta(t.all, before + it.n_tiles - 1, n);
-    }
+  const int64_t before = spot.at;
+  const AttnItem it = spot.info;
+  if (split) {
+    c0 = line_cta(t.all, before, n);
+    c1 = line_cta(t.all, before + it.n_tiles - 1, n);
     split = c0 != c1;
   }
   cudaGridDependencySynchronize();       // the partial results are complete and visible
@@ -117,6 +117,24 @@ __global__ void __launch_bounds__(kMergeThreads)
       }
     } else {
       for (int row = blockIdx.y; row < it.rows; row += gridDim.y) {
+        // this warp's first parts are requested before the maximum is known
+        constexpr int AHEAD = 3;
+        RowPart<D> x[AHEAD];
+        float2 xl[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+          const int i = warp + k * kMergeWarps;
+          if (i < parts) {
+            const int64_t slot = part(i) + row;
+            xl[k] = ml[slot];
+#pragma unroll
+            for (int e = 0; e < D / 128; ++e)
+              x[k].v[e] = reinterpret_cast<const float4*>(o + slot * D)[lane + 32 * e];
+          } else {
+            xl[k] = make_float2(-INFINITY, 0.f);
+            x[k] = {};
+          }
+        }
         float M = -INFINITY;
         for (int i = lane; i < parts; i += 32) M = fmax_nan(M, ml[part(i) + row].x);
 #pragma unroll
@@ -124,12 +142,26 @@ __global__ void __launch_bounds__(kMergeThreads)
         const float sub = M == -INFINITY ? 0.f : M;
         RowPart<D> acc = {};
         float L = 0.f;
-#pragma unroll 4
-        for (int i = warp; i < parts; i += kMergeWarps) {
-          const float2 x = ml[part(i) + row];
-          const float f = exp2f(x.x - sub);
-          L = fmaf(x.y, f, L);
-          add_part<D>(acc, o + (part(i) + row) * D, f);
+        auto add = [&](const RowPart<D>& p, float2 v) {
+          const float f = exp2f(v.x - sub);
+          L = fmaf(v.y, f, L);
+#pragma unroll
+          for (int e = 0; e < D / 128; ++e) {
+            acc.v[e].x = fmaf(p.v[e].x, f, acc.v[e].x);
+            acc.v[e].y = fmaf(p.v[e].y, f, acc.v[e].y);
+            acc.v[e].z = fmaf(p.v[e].z, f, acc.v[e].z);
+            acc.v[e].w = fmaf(p.v[e].w, f, acc.v[e].w);
+          }
+        };
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) add(x[k], xl[k]);
+        for (int i = warp + AHEAD * kMergeWarps; i < parts; i += kMergeWarps) {
+          const int64_t slot = part(i) + row;
+          RowPart<D> y;
+#pragma unroll
+          for (int e = 0; e < D / 128; ++e)
+            y.v[e] = reinterpret_cast<const float4*>(o + slot * D)[lane + 32 * e];
+          add(y, ml[slot]);
         }
         acc_s[warp][lane] = acc;
         if (lane == 0) l_s[warp] = L;
@@ -191,11 +223,10 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
 // for them; beyond, the tensor-memory kernel, whose tiles hold 128.
 static bool few_rows(int n_q, int G) { return static_cast<int64_t>(n_q) * G <= 16; }
 
-size_t cache_attn_ws_bytes(int64_t units, int G, int n_q, int d, int format) {
-  (void)units;
-  return few_rows(n_q, G)
-             ? attn_ws_bytes(rows_ctas(format, d), rows_block(static_cast<int64_t>(n_q) * G), d)
-             : attn_ws_bytes(kTcCtas, tc_block(d), d);
+size_t cache_attn_ws_bytes(int G, int n_q, int d, int format) {
+  if (!few_rows(n_q, G)) return attn_ws_bytes(kTcCtas, tc_block(d), d);
+  const int block = rows_block(static_cast<int64_t>(n_q) * G);
+  return attn_ws_bytes(rows_ctas(format, d, block), block, d);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t s, int* launches) {

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ int64_t scratch[THREADS / 32];
-  __shared__ int64_t found[2];
+  __shared__ LineSpot spot_s;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Cfg::OFF_BAR);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = kv_full + STAGES;
@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
   const int64_t cta = blockIdx.x;
 
   cudaTriggerProgrammaticLaunchCompletion();   // the merge may be launched; it waits for this grid
-  Line<THREADS> line(a.c, shape, items, scratch, found);
+  Line<THREADS> line(a.c, shape, items, scratch, &spot_s);
   const int64_t all = line.all;
   const int64_t n_cta = line_ctas(all, gridDim.x);
   if (cta >= n_cta) return;
   const int64_t p0 = line_cut(all, cta, n_cta), p1 = line_cut(all, cta + 1, n_cta);
-  int64_t w_first, w_first_at;
-  line.find(p0, &w_first, &w_first_at);
+  const LineSpot spot = line.find(p0);
+  const int64_t w_first = spot.item, w_first_at = spot.at;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {

@@ -51,34 +51,44 @@ __device__ __forceinline__ AttnItem attn_item(const CacheArgs& c, const AttnShap
   return it;
 }
 
-// The line as the THREADS threads of a block see it: `sums` (THREADS / 32 entries)
-// and `found` (2) are shared scratch.  Up to THREADS items are loaded once, one per
-// thread; more are walked again for every question.
+// An item as the thread that counted its tiles hands it to the block.
+struct LineSpot {
+  int64_t item, at;      // the item and the place of its first tile
+  AttnItem info;
+};
+
+// The line as the THREADS threads of a block see it; `sums` (THREADS / 32 entries) and
+// `spot` are shared scratch.  Up to THREADS items are loaded once, one per thread, and
+// a spot costs one barrier; more are walked again for every question.
 template <int THREADS>
 struct Line {
   const CacheArgs& c;
   const AttnShape& s;
   int64_t items;
   int64_t* sums;
-  int64_t* found;
+  LineSpot* spot;
   int64_t all;         // tiles of all items
   int64_t mine_end;    // items <= THREADS: tiles up to and with item threadIdx.x
-  int mine;            // its own
+  AttnItem mine;
 
   __device__ Line(const CacheArgs& c_, const AttnShape& s_, int64_t items_, int64_t* sums_,
-                  int64_t* found_)
-      : c(c_), s(s_), items(items_), sums(sums_), found(found_), all(0), mine_end(0), mine(0) {
+                  LineSpot* spot_)
+      : c(c_), s(s_), items(items_), sums(sums_), spot(spot_), all(0), mine_end(0) {
+    int64_t v = 0;
     if (items <= THREADS) {
-      mine = threadIdx.x < items ? attn_item(c, s, threadIdx.x).n_tiles : 0;
-      mine_end = scan(mine, &all);
+      if (threadIdx.x < items) {
+        mine = attn_item(c, s, threadIdx.x);
+        v = mine.n_tiles;
+      }
+      mine_end = scan(v, &all);
     } else {
-      int64_t v = 0;
       for (int64_t i = threadIdx.x; i < items; i += THREADS) v += attn_item(c, s, i).n_tiles;
       scan(v, &all);
     }
   }
 
-  // Inclusive prefix sum over the block's threads, and the total.
+  // Inclusive prefix sum over the block's threads, and the total.  Two calls need a
+  // barrier between them.
   __device__ int64_t scan(int64_t v, int64_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -86,7 +96,6 @@ struct Line {
       const int64_t o = __shfl_up_sync(0xffffffffu, v, k);
       if (lane >= k) v += o;
     }
-    __syncthreads();
     if (lane == 31) sums[warp] = v;
     __syncthreads();
     int64_t t = 0;
@@ -99,48 +108,43 @@ struct Line {
     return v;
   }
 
-  // The item that holds tile p (0 <= p < all) and the place of its first tile.
-  __device__ void find(int64_t p, int64_t* item, int64_t* at) {
+  // The spot of tile p (0 <= p < all); one use per block.
+  __device__ LineSpot find(int64_t p) {
     if (items <= THREADS) {
-      if (mine > 0 && mine_end - mine <= p && p < mine_end) {
-        found[0] = threadIdx.x;
-        found[1] = mine_end - mine;
-      }
+      if (threadIdx.x < items && mine_end - mine.n_tiles <= p && p < mine_end)
+        *spot = LineSpot{static_cast<int64_t>(threadIdx.x), mine_end - mine.n_tiles, mine};
     } else {
       int64_t base = 0;
       for (int64_t i0 = 0; i0 < items; i0 += THREADS) {
         const int64_t i = i0 + threadIdx.x;
-        const int t = i < items ? attn_item(c, s, i).n_tiles : 0;
+        AttnItem it;
+        it.n_tiles = 0;
+        if (i < items) it = attn_item(c, s, i);
         int64_t sum;
-        const int64_t end = base + scan(t, &sum);
-        if (t > 0 && end - t <= p && p < end) {
-          found[0] = i;
-          found[1] = end - t;
-        }
+        __syncthreads();
+        const int64_t end = base + scan(it.n_tiles, &sum);
+        if (end - it.n_tiles <= p && p < end) *spot = LineSpot{i, end - it.n_tiles, it};
         base += sum;
         if (base > p) break;      // the same for every thread
       }
     }
     __syncthreads();
-    *item = found[0];
-    *at = found[1];
-    __syncthreads();
+    return *spot;
   }
 
-  // Tiles before item w.
-  __device__ int64_t before(int64_t w) {
+  // The spot of item w; one use per block.
+  __device__ LineSpot of_item(int64_t w) {
     if (items <= THREADS) {
-      if (threadIdx.x == w) found[0] = mine_end - mine;
+      if (threadIdx.x == w) *spot = LineSpot{w, mine_end - mine.n_tiles, mine};
     } else {
       int64_t v = 0, sum;
       for (int64_t i = threadIdx.x; i < w; i += THREADS) v += attn_item(c, s, i).n_tiles;
+      __syncthreads();
       scan(v, &sum);
-      if (threadIdx.x == 0) found[0] = sum;
+      if (threadIdx.x == 0) *spot = LineSpot{w, sum, attn_item(c, s, w)};
     }
     __syncthreads();
-    const int64_t r = found[0];
-    __syncthreads();
-    return r;
+    return *spot;
   }
 };
 
@@ -149,9 +153,15 @@ struct Line {
 __device__ __forceinline__ int64_t line_ctas(int64_t all, int64_t grid) {
   return all < grid ? all : grid;
 }
+// a / b for a, b >= 0: 32-bit division where it will do (a 64-bit one is a few
+// hundred instructions, which show in a decoding step).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 // Piece of the line that CTA i of n takes: [line_cut(i), line_cut(i + 1)).
 __device__ __forceinline__ int64_t line_cut(int64_t all, int64_t i, int64_t n) {
-  return all * i / n;
+  return quotient(all * i, n);
 }
 // Slot of CTA i's part of the item whose tiles begin at `before` on the line.
 __device__ __forceinline__ int64_t line_slot(int64_t all, int64_t i, int64_t n, int64_t before) {
@@ -159,7 +169,7 @@ __device__ __forceinline__ int64_t line_slot(int64_t all, int64_t i, int64_t n, 
 }
 // The CTA that takes tile p.
 __device__ __forceinline__ int64_t line_cta(int64_t all, int64_t p, int64_t n) {
-  int64_t i = p * n / all;
+  int64_t i = quotient(p * n, all);
   while (i + 1 < n && line_cut(all, i + 1, n) <= p) ++i;
   while (i > 0 && line_cut(all, i, n) > p) --i;
   return i;

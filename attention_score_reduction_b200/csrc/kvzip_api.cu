@@ -570,7 +570,7 @@ size_t kvzip_cache_attention_workspace_size(const kvzip_cache* cache, int G, int
   kvzip::CacheArgs c;
   if (cache_args(cache, &c) != KVZIP_OK || G <= 0 || G > kMaxG || n_q < 0) return 0;
   if (cache->units == 0 || n_q == 0) return 0;
-  return kvzip::cache_attn_ws_bytes(c.units, G, n_q, c.d, c.format);
+  return kvzip::cache_attn_ws_bytes(G, n_q, c.d, c.format);
 }
 
 kvzip_status kvzip_cache_attention(const kvzip_cache* cache, const void* q, int64_t q_unit_stride,

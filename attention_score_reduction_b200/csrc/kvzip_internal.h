@@ -176,7 +176,7 @@ struct CacheAttnArgs {
   uint64_t timeout_ns;
   int test_stall;
 };
-size_t cache_attn_ws_bytes(int64_t units, int G, int n_q, int d, int format);
+size_t cache_attn_ws_bytes(int G, int n_q, int d, int format);
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t s, int* launches);
 
 // Records the launch count of an accepted call (read by kvzip_last_launch_count).
