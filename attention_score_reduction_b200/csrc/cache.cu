@@ -29,6 +29,7 @@
 
 #include "cache.cuh"
 #include "kvzip_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace kvzip {
 
@@ -73,146 +74,218 @@ __device__ __forceinline__ void advance_len(const CacheWriteArgs& a, int64_t u, 
   a.c.lens[u] = held_to(first + rows_of(a, u), cap, a.c.status);
 }
 
-template <int LPR>
-__device__ __forceinline__ float row_max(float v) {
-#pragma unroll
-  for (int w = LPR / 2; w >= 1; w >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, w));
-  return v;
-}
-
-// Stores this lane's eight elements (four bf16 pairs) of a row.
-template <int FMT, int D>
-__device__ __forceinline__ void store_row(uint8_t* pages, uint32_t* params, int64_t slot, int lr,
-                                          const uint4 raw, bool live) {
-  constexpr int LPR = D / 8;
-  if constexpr (FMT == kFmtBf16) {
-    if (live)
-      *reinterpret_cast<uint4*>(pages + slot * CacheRow<FMT, D>::BYTES + lr * 16) = raw;
-    return;
-  }
-  float x[8];
+// One row's eight elements of a lane, as floats.
+__device__ __forceinline__ void unpack8(const uint4& raw, float (&x)[8]) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[2 * i] = bf16_lo(w[i]);
     x[2 * i + 1] = bf16_hi(w[i]);
   }
-  if constexpr (FMT == kFmtFp8) {
+}
+
+// What the 4-bit codes of a row are computed with.
+struct Int4Row {
+  uint32_t par;
+  float lift, zl, s, inv;
+  bool exact;             // the row needs int4_codes<true>
+};
+
+__device__ __forceinline__ Int4Row int4_row(float lo, float hi) {
+  Int4Row q;
+  const bool bad = !(hi < kInt4Limit && lo > -kInt4Limit);      // infinity, NaN, too large
+  q.par = bad ? 0x7fc07fc0u : pack_bf16x2((hi - lo) / 15.f, lo);
+  q.s = bf16_lo(q.par);
+  // tiny scales are lifted by 2^100 (exactly), so that 1 / s stays finite
+  q.lift = q.s < 8.6736174e-19f ? 1.2676506e30f : 1.f;
+  q.zl = -lo * q.lift;
+  q.s *= q.lift;
+  q.inv = q.s > 0.f ? 1.f / q.s : 0.f;
+  // x - z is exact in 32 bits unless one of the two is below 2^-16 of the other.  Then
+  // it is the other, rounded, and that matters only where the other is half way between
+  // two codes: -z by itself, or any x beside a tiny z.
+  const float zq = q.zl * q.inv, frac = zq - floorf(zq);
+  q.exact = q.lift > 1.f || fabsf(frac - 0.5f) < 1e-4f + fabsf(zq) * 4.7683716e-7f || (lo != 0.f && fabsf(lo) < hi * 3.0517578e-5f);
+  return q;
+}
+
+// Eight codes as a word.  The quotient is corrected by its exact remainder, so that a
+// tie is a tie (of bf16 rows a few elements in a thousand are: x, z and s have eight
+// significant bits each; by the same count any other quotient is at least 2^-13 from
+// a border).  Rounded to even by adding 1.5 * 2^23: the code is in the sum's low bits.
+// A quotient is between 0 and 15.06, as s is within 2^-8 of range / 15.
+// EXACT: a tiny s, a subnormal bf16, can be further off (codes are held to 15), and
+// where x - z was rounded its error decides a tie.
+template <bool EXACT>
+__device__ __forceinline__ uint32_t int4_codes(const uint4& raw, const Int4Row& q) {
+  constexpr float kRound = 12582912.f;
+  constexpr uint32_t kRoundBits = 0x4b400000u;
+  float x[8];
+  unpack8(raw, x);
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float d = fmaf(x[i], q.lift, q.zl);               // x - z
+    float t = d * q.inv;
+    t = fmaf(fmaf(-t, q.s, d), q.inv, t);
+    float u = t + kRound;
+    if constexpr (EXACT) {
+      const float r = fmaf(kRound - u, q.s, d), half = 0.5f * q.s;
+      const bool odd = __float_as_uint(u) & 1u;
+      const float a = x[i] * q.lift, bb = d - a;
+      const float err = (a - (d - bb)) + (q.zl - bb);
+      if (r > half || (r == half && (err > 0.f || (err == 0.f && odd)))) u += 1.f;
+      if (r < -half || (r == -half && (err < 0.f || (err == 0.f && odd)))) u -= 1.f;
+      u = fminf(u, kRound + 15.f);
+    }
+    word += (__float_as_uint(u) - kRoundBits) << (4 * i);
+  }
+  return q.s > 0.f ? word : 0u;
+}
+
+// Stores N rows of which this lane has eight elements each; slot < 0: none.  Every step
+// goes over all rows before the next, so that their latencies overlap.
+template <int FMT, int D, int N>
+__device__ __forceinline__ void store_rows(uint8_t* pages, uint32_t* params, const int64_t (&slot)[N],
+                                           int lr, const uint4 (&raw)[N]) {
+  constexpr int LPR = D / 8;
+  if constexpr (FMT == kFmtBf16) {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (slot[n] >= 0)
+        *reinterpret_cast<uint4*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + lr * 16) = raw[n];
+  } else if constexpr (FMT == kFmtFp8) {
     // the largest magnitude by the order of the bits, where a NaN ranks above
     // infinity and so is seen
-    uint32_t top = 0;
+    uint32_t top[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      top = max(top, (w[i] << 16) & 0x7fff0000u);
-      top = max(top, w[i] & 0x7fff0000u);
+    for (int n = 0; n < N; ++n) {
+      const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+      uint32_t t = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t = max(t, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+      top[n] = t;
     }
 #pragma unroll
-    for (int k = LPR / 2; k >= 1; k >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
-    // 448 * 2^e = 1.75 * 2^(e + 8): e from the exponent, one more above 1.75
-    int e = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
-    e = top == 0 ? 0 : max(e, -126);
-    const bool bad = top >= 0x7f800000u;
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);   // 2^-e
-    uint32_t c[4];
+    for (int k = LPR / 2; k >= 1; k >>= 1)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = pack_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-    if (live) {
-      // a bad row's codes are zeros: NaN lives in parameters only, which the
-      // attention applies after its mask
-      *reinterpret_cast<uint2*>(pages + slot * CacheRow<FMT, D>::BYTES + lr * 8) =
-          bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-      if (lr == 0)
-        params[slot] = bad ? 0x7fc00000u : static_cast<uint32_t>(127 + e) << 23;
+      for (int n = 0; n < N; ++n) top[n] = max(top[n], __shfl_xor_sync(0xffffffffu, top[n], k));
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      // 448 * 2^e = 1.75 * 2^(e + 8): e from the exponent, one more above 1.75
+      int e = static_cast<int>(top[n] >> 23) - 127 - 8 + ((top[n] & 0x7fffffu) > 0x600000u ? 1 : 0);
+      e = top[n] == 0 ? 0 : max(e, -126);
+      const bool bad = top[n] >= 0x7f800000u;
+      const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);   // 2^-e
+      float x[8];
+      unpack8(raw[n], x);
+      uint32_t c[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = pack_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+      if (slot[n] >= 0) {
+        // a bad row's codes are zeros: NaN lives in parameters only, which the
+        // attention applies after its mask
+        *reinterpret_cast<uint2*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + lr * 8) =
+            bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        if (lr == 0)
+          params[slot[n]] = bad ? 0x7fc00000u : static_cast<uint32_t>(127 + e) << 23;
+      }
     }
   } else {
-    float lo = x[0], hi = x[0];
-    bool bad = false;
+    float lo[N], hi[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      lo = fminf(lo, x[i]);
-      hi = fmaxf(hi, x[i]);
-      bad |= !(fabsf(x[i]) < kInt4Limit);
+    for (int n = 0; n < N; ++n) {
+      float x[8];
+      unpack8(raw[n], x);
+      lo[n] = fmin3_nan(fmin3_nan(x[0], x[1], x[2]), fmin3_nan(x[3], x[4], x[5]), fmin_nan(x[6], x[7]));
+      hi[n] = fmax3_nan(fmax3_nan(x[0], x[1], x[2]), fmax3_nan(x[3], x[4], x[5]), fmax_nan(x[6], x[7]));
     }
-    lo = -row_max<LPR>(-lo);
-    hi = row_max<LPR>(hi);
-    const uint32_t votes = __ballot_sync(0xffffffffu, bad);
-    bad = LPR == 32 ? votes != 0
-                    : ((votes >> (threadIdx.x & 16)) & 0xffffu) != 0;
-    const uint32_t par = bad ? 0x7fc07fc0u : pack_bf16x2((hi - lo) / 15.f, lo);
-    float s = bf16_lo(par);
-    // tiny scales are lifted by 2^100 (exactly), so that 1 / s stays finite
-    const float lift = s < 8.6736174e-19f ? 1.2676506e30f : 1.f;
-    const float zl = -lo * lift;
-    s *= lift;
-    const float inv = s > 0.f ? 1.f / s : 0.f;
-    const float half = s > 0.f ? 0.5f * s : INFINITY;
-    uint32_t code[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = fmaf(x[i], lift, zl);      // x - z, rounded once
-      int c = __float2int_rn(d * inv);
-      const float r = fmaf(static_cast<float>(-c), s, d);   // exact: |r| is at most about s / 2
-      if (fabsf(r) >= 0.4999f * s) {
-        // next to a border between two codes: settle it with the error of d
-        const float a = x[i] * lift, bb = d - a;
-        const float err = (a - (d - bb)) + (zl - bb);
-        if (r > half || (r == half && (err > 0.f || (err == 0.f && (c & 1))))) ++c;
-        if (r < -half || (r == -half && (err < 0.f || (err == 0.f && (c & 1))))) --c;
+    for (int k = LPR / 2; k >= 1; k >>= 1)
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        lo[n] = fmin_nan(lo[n], __shfl_xor_sync(0xffffffffu, lo[n], k));
+        hi[n] = fmax_nan(hi[n], __shfl_xor_sync(0xffffffffu, hi[n], k));
       }
-      code[i] = static_cast<uint32_t>(min(max(c, 0), 15));
-    }
-    if (live) {
-      uint32_t word = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) word |= code[i] << (4 * i);
-      *reinterpret_cast<uint32_t*>(pages + slot * CacheRow<FMT, D>::BYTES + lr * 4) = word;
-      if (lr == 0) params[slot] = par;
+    for (int n = 0; n < N; ++n) {
+      const Int4Row q = int4_row(lo[n], hi[n]);
+      uint32_t word = int4_codes<false>(raw[n], q);
+      if (q.exact) word = int4_codes<true>(raw[n], q);
+      if (slot[n] >= 0) {
+        *reinterpret_cast<uint32_t*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + lr * 4) = word;
+        if (lr == 0) params[slot[n]] = q.par;
+      }
     }
   }
 }
 
-// This lane's eight elements of a stored row as four bf16 pairs.
+// Codes of eight elements of a stored row as loaded, and as four bf16 pairs.
+template <int FMT>
+struct RowBits {
+  uint4 c;         // bf16: 16 bytes; fp8: 8 in x, y; int4: 4 in x
+  uint32_t par;
+};
 template <int FMT, int D>
-__device__ __forceinline__ uint4 load_row(const uint8_t* pages, const uint32_t* params, int64_t slot,
-                                          int lr, bool live) {
-  if (!live) return make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ RowBits<FMT> load_row(const uint8_t* pages, const uint32_t* params,
+                                                 int64_t slot, int lr) {
+  RowBits<FMT> b{};
   const uint8_t* p = pages + slot * CacheRow<FMT, D>::BYTES;
   if constexpr (FMT == kFmtBf16) {
-    return ldg_stream16(p + lr * 16);
+    b.c = ldg_stream16(p + lr * 16);
+  } else {
+    if constexpr (FMT == kFmtFp8) {
+      const uint2 v = ldg_stream8(p + lr * 8);
+      b.c.x = v.x;
+      b.c.y = v.y;
+    } else {
+      b.c.x = __ldg(reinterpret_cast<const uint32_t*>(p + lr * 4));
+    }
+    b.par = __ldg(params + slot);
+  }
+  return b;
+}
+template <int FMT>
+__device__ __forceinline__ uint4 row_values(const RowBits<FMT>& b) {
+  if constexpr (FMT == kFmtBf16) {
+    return b.c;
   } else if constexpr (FMT == kFmtFp8) {
-    const uint2 c = ldg_stream8(p + lr * 8);
-    const float s = __uint_as_float(params[slot]);
-    uint32_t o[4];
+    const float s = __uint_as_float(b.par);
+    uint32_t h[4], o[4];
+    e4m3x4_f16x2(b.c.x, h[0], h[1]);
+    e4m3x4_f16x2(b.c.y, h[2], h[3]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t h = e4m3x2_f16x2(i < 2 ? c.x >> (16 * i) : c.y >> (16 * (i - 2)));
       float f0, f1;
       asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\t"
           "cvt.f32.f16 %1, b;\n\t}"
           : "=f"(f0), "=f"(f1)
-          : "r"(h));
+          : "r"(h[i]));
       o[i] = pack_bf16x2(f0 * s, f1 * s);   // exact: 4 significant bits and a power of two
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
   } else {
-    const uint32_t c = *reinterpret_cast<const uint32_t*>(p + lr * 4);
-    const uint32_t par = params[slot];
-    const float s = bf16_lo(par), z = bf16_hi(par);
+    const uint32_t s2 = __byte_perm(b.par, 0, 0x1010), z2 = __byte_perm(b.par, 0, 0x3232);
+    // 0x4300 | c is the bf16 128 + c; minus 128 it is exact, and s c + z is rounded once
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      o[i] = pack_bf16x2(fmaf(static_cast<float>((c >> (8 * i)) & 15u), s, z),
-                         fmaf(static_cast<float>((c >> (8 * i + 4)) & 15u), s, z));
-    return make_uint4(o[0], o[1], o[2], o[3]);
+      o[i] = bfma2(bfma2(and_or(b.c.x >> (4 * i), 0x000f000fu, 0x43004300u), 0x3f803f80u, 0xc300c300u),
+                   s2, z2);                       // elements i and i + 4
+    return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410),
+                      __byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
   }
 }
 
 // mode 0: lens left to another launch; 1: starts and lens are different buffers,
 // any thread may write lens; 2: append, a warp's chunk is one whole unit.
+// Rows that are not there load from the first row instead (no branch between loads).
+// Two rows of K and of V per step: at four the 4-bit kernel spills or loses half of
+// its warps (62000-row fill, int4: 58 us; four rows 65; next rows requested ahead 61).
 template <int FMT, int D>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 4)
     cache_write_rows(const CacheWriteArgs a, int64_t total, int chunk, int mode) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, UNR = 4;
+  constexpr int LPR = D / 8, RPW = 32 / LPR, UNR = 2;
   const int lane = threadIdx.x & 31;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   if (mode == 1) {
@@ -252,23 +325,12 @@ __global__ void __launch_bounds__(kRowThreads)
     for (int j = 0; j < UNR; ++j) {
       const int i = i0 + j * RPW + sub;          // i >= chunk: its lane holds slot = -1, or i >= 32
       sl[j] = __shfl_sync(0xffffffffu, slot, i & 31);
-      const int64_t ks = __shfl_sync(0xffffffffu, ksrc, i & 31);
-      const int64_t vs = __shfl_sync(0xffffffffu, vsrc, i & 31);
+      kr[j] = ldg_stream16(kp + __shfl_sync(0xffffffffu, ksrc, i & 31));
+      vr[j] = ldg_stream16(vp + __shfl_sync(0xffffffffu, vsrc, i & 31));
       if (i >= chunk) sl[j] = -1;
-      if (sl[j] >= 0) {
-        kr[j] = ldg_stream16(kp + ks);
-        vr[j] = ldg_stream16(vp + vs);
-      } else {
-        kr[j] = vr[j] = make_uint4(0, 0, 0, 0);
-      }
     }
-#pragma unroll
-    for (int j = 0; j < UNR; ++j) {
-      store_row<FMT, D>(static_cast<uint8_t*>(a.c.k_pages), a.c.k_params, sl[j], lr, kr[j],
-                        sl[j] >= 0);
-      store_row<FMT, D>(static_cast<uint8_t*>(a.c.v_pages), a.c.v_params, sl[j], lr, vr[j],
-                        sl[j] >= 0);
-    }
+    store_rows<FMT, D, UNR>(static_cast<uint8_t*>(a.c.k_pages), a.c.k_params, sl, lr, kr);
+    store_rows<FMT, D, UNR>(static_cast<uint8_t*>(a.c.v_pages), a.c.v_params, sl, lr, vr);
   }
 }
 
@@ -281,7 +343,8 @@ __global__ void cache_advance(const CacheWriteArgs a) {
 template <int FMT, int D>
 __global__ void __launch_bounds__(kRowThreads)
     cache_read_rows(const CacheReadArgs a, int64_t total, int chunk) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, UNR = 4;
+  // rows in flight: more where a row is few bytes
+  constexpr int LPR = D / 8, RPW = 32 / LPR, UNR = FMT == kFmtInt4 ? 8 : 4;
   const int lane = threadIdx.x & 31;
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   const int64_t r0 = warp * chunk;
@@ -299,23 +362,24 @@ __global__ void __launch_bounds__(kRowThreads)
   const int sub = lane / LPR, lr = lane % LPR;
   for (int i0 = 0; i0 < chunk; i0 += UNR * RPW) {
     int64_t sl[UNR];
-    uint4 kr[UNR], vr[UNR];
+    RowBits<FMT> kb[UNR], vb[UNR];
 #pragma unroll
     for (int j = 0; j < UNR; ++j) {
       const int i = i0 + j * RPW + sub;
       sl[j] = __shfl_sync(0xffffffffu, slot, i & 31);
       if (i >= chunk) sl[j] = -1;
-      kr[j] = load_row<FMT, D>(static_cast<const uint8_t*>(a.c.k_pages), a.c.k_params, sl[j], lr,
-                               sl[j] >= 0);
-      vr[j] = load_row<FMT, D>(static_cast<const uint8_t*>(a.c.v_pages), a.c.v_params, sl[j], lr,
-                               sl[j] >= 0);
+      const int64_t at = sl[j] < 0 ? 0 : sl[j];       // rows that are not there: no branch
+      kb[j] = load_row<FMT, D>(static_cast<const uint8_t*>(a.c.k_pages), a.c.k_params, at, lr);
+      vb[j] = load_row<FMT, D>(static_cast<const uint8_t*>(a.c.v_pages), a.c.v_params, at, lr);
     }
 #pragma unroll
     for (int j = 0; j < UNR; ++j) {
-      if (sl[j] < 0) continue;
-      const int64_t o = (r0 + i0 + j * RPW + sub) * D + lr * 8;
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_out) + o) = kr[j];
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_out) + o) = vr[j];
+      const uint4 kv = row_values<FMT>(kb[j]), vv = row_values<FMT>(vb[j]);
+      if (sl[j] >= 0) {
+        const int64_t o = (r0 + i0 + j * RPW + sub) * D + lr * 8;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_out) + o) = kv;
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_out) + o) = vv;
+      }
     }
   }
 }

@@ -100,6 +100,11 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
+__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 // Nibbles 0 and 4 (NIB = 0) or 1 and 5 (NIB = 1) of w as exact f16x2 codes:
 // 0x6400 | c is 1024 + c, 0x6400 | 16 c is 1024 + 16 c.
 template <int NIB>
