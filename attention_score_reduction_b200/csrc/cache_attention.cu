@@ -96,7 +96,7 @@ struct RowsCfg {
   static constexpr int KS = D / 16;                       // k-steps of the logits; m-tiles of the output
   static constexpr bool QUANT = FMT != kFmtBf16;
   // a warp's ring of batches: K codes, V codes, K parameters, V parameters
-  static constexpr int SLOTS = RB >= 256 && D == 128 ? 2 : (FMT == kFmtFp8 && D == 128 ? 2 : 3);
+  static constexpr int SLOTS = FMT == kFmtFp8 && D == 128 ? 2 : 3;
   static constexpr int CODES = BR * RB;
   static constexpr int SLOT = 2 * CODES + (QUANT ? 8 * BR : 0);
   static constexpr int RING = WARPS * SLOTS * SLOT;
@@ -120,6 +120,12 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) 
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {
@@ -128,7 +134,7 @@ __device__ __forceinline__ void copies_wait() {
 
 // CTAs that fit on an SM together, by registers and shared memory.
 constexpr int rows_per_sm(int format, int d, int block) {
-  if (d == 128) return block == 8 ? (format == kFmtInt4 ? 4 : 3) : 2;
+  if (d == 128) return block == 8 && format != kFmtBf16 ? 3 : 2;
   return format == kFmtBf16 ? 1 : 2;
 }
 
@@ -180,13 +186,38 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
     constexpr int GROUPS = BR / 16;
     // pool row of each 16-row group of a batch, or -1
     auto find = [&](int r, int64_t (&base)[GROUPS]) {
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g)
-        base[g] = r + 16 * g < r_end ? cache_slot(a.c, it.u, r + 16 * g) : -1;
+      base[0] = r < r_end ? cache_slot(a.c, it.u, r) : -1;
+      if constexpr (GROUPS > 1) {
+        if (a.c.page_shift >= 5) base[1] = base[0] >= 0 ? base[0] + 16 : -1;   // the same page
+        else base[1] = r + 16 < r_end ? cache_slot(a.c, it.u, r + 16) : -1;
+      }
     };
     // batch of rows r .. into a slot; rows past the end and of a bad page become zeros
     auto request = [&](int r, uint32_t slot, const int64_t (&base)[GROUPS]) {
       constexpr int CPR = RB / 16, PER = 32 / CPR > 0 ? 32 / CPR : 1;   // chunks a row, rows a copy
+      if (r + BR <= r_end && base[0] >= 0 && base[GROUPS - 1] >= 0) {
+        // nothing to leave out: a copy takes 512 consecutive bytes of a group
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+          const uint8_t* k = static_cast<const uint8_t*>(a.c.k_pages) + base[g] * RB + 16 * lane;
+          const uint8_t* v = static_cast<const uint8_t*>(a.c.v_pages) + base[g] * RB + 16 * lane;
+#pragma unroll
+          for (int i = 0; i < RB / 32; ++i) {
+            const int idx = 32 * (i + g * (RB / 32)) + lane, row = idx / CPR, chunk = idx % CPR;
+            const uint32_t dst = slot + row * RB + 16 * swizzled<RB>(row, chunk);
+            copy16(dst, k + 512 * i);
+            copy16(dst + Cfg::CODES, v + 512 * i);
+          }
+        }
+        if constexpr (QUANT) {
+          if (lane < BR) {
+            const int64_t at = (BR > 16 && lane >= 16 ? base[GROUPS - 1] : base[0]) + (lane & 15);
+            copy4(slot + 2 * Cfg::CODES + 4 * lane, a.c.k_params + at);
+            copy4(slot + 2 * Cfg::CODES + 4 * (BR + lane), a.c.v_params + at);
+          }
+        }
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < Cfg::CODES / 512; ++i) {
         const int idx = 32 * i + lane, row = idx / CPR, chunk = idx % CPR;
@@ -283,22 +314,38 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
       }
     }
 
-    // State of the query rows this lane has in the logits: running maximum m and sum l
-    // (this lane's columns); quantised: weights p s are formed as fp16 relative to a
-    // power of two, a = p s F, with the largest so far, top_a, kept within 2^-2 .. 2^12;
-    // int4: oz = sum p z.
-    float m[NT], l[NT], F[NT], top_a[NT], oz[NT];
+    // State of the query rows this lane has in the logits.  Weights are p = 2^(x - m) with
+    // a reference m that follows a row's running maximum only once that is 2^30 above it
+    // (32-bit sums bear it): no exchange between lanes and no rescaling in most batches.
+    // l: this lane's sums of p, by column parity.  Quantised: weights p s are formed as
+    // fp16 times a power of two F; F moves when one exceeds top, or (none so far, top = 0)
+    // at the first; lead: the largest p s at the last move.  int4: oz = sum p z.
+    float m[NT], F[NT], lead[NT], top[NT];
+    float2 l2[NT], oz2[NT];
     float o[NT][KS][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       m[t] = -INFINITY;
-      l[t] = oz[t] = top_a[t] = 0.f;
+      l2[t] = oz2[t] = make_float2(0.f, 0.f);
+      lead[t] = top[t] = 0.f;
       F[t] = 1.f;
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][k][e] = 0.f;
     }
+    // multiplies row t's output by f (of the lanes that have the row in the logits)
+    auto rescale = [&](int t, float f) {
+      const float f_lo = __shfl_sync(0xffffffffu, f, 8 * qp);
+      const float f_hi = __shfl_sync(0xffffffffu, f, 8 * qp + 4);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        o[t][k][0] *= f_lo;
+        o[t][k][1] *= f_hi;
+        o[t][k][2] *= f_lo;
+        o[t][k][3] *= f_hi;
+      }
+    };
 
     int n_slot = 0;
     for (int r = r_first; r < r_end; r += WARPS * BR) {
@@ -348,104 +395,99 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
           vpar[j] = lds8(slot + 2 * Cfg::CODES + 4 * (BR + 8 * j + 2 * qp));
         }
       }
-      // ---- logits (log2 domain) in place, their maximum, weights
-      float scale_o[NT];
+      // ---- logits (log2 domain) in place, weights
       uint32_t phi[NT][NJ], plo[NT][QUANT ? 1 : NJ];
-      bool moved = false;
       auto softmax = [&](auto mask_tag) {
         constexpr bool MASK = decltype(mask_tag)::value;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+          float2 x[NJ];
           float mx = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = s[j][2 * t + e];
-              const uint32_t par = QUANT ? (e ? kpar[j].y : kpar[j].x) : 0u;
-              if constexpr (FMT == kFmtFp8) x *= __uint_as_float(par) * cq[t];
-              else if constexpr (FMT == kFmtInt4) x = fmaf(x, bf16_lo(par) * cq[t], bf16_hi(par) * cz[t]);
-              else x *= cq[t];
-              if (MASK) x = r + 8 * j + 2 * qp + e < lim[t] ? x : -INFINITY;
-              mx = fmaxf(mx, x);
+          for (int j = 0; j < NJ; ++j) {
+            x[j] = make_float2(s[j][2 * t], s[j][2 * t + 1]);
+            const float2 c2 = make_float2(cq[t], cq[t]);
+            if constexpr (FMT == kFmtFp8) {
+              x[j] = fmul2(x[j], fmul2(make_float2(__uint_as_float(kpar[j].x),
+                                                   __uint_as_float(kpar[j].y)), c2));
+            } else if constexpr (FMT == kFmtInt4) {
+              const float2 sc = fmul2(make_float2(bf16_lo(kpar[j].x), bf16_lo(kpar[j].y)), c2);
+              const float2 zc = fmul2(make_float2(bf16_hi(kpar[j].x), bf16_hi(kpar[j].y)),
+                                      make_float2(cz[t], cz[t]));
+              x[j] = ffma2(x[j], sc, zc);
+            } else {
+              x[j] = fmul2(x[j], c2);
             }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float m_new = fmaxf(m[t], mx);
-          const float m_sub = m_new == -INFINITY ? 0.f : m_new;   // nothing seen yet
-          const float alpha = ex2_approx(m[t] - m_sub);
-          moved |= m_new != m[t];
-          m[t] = m_new;
-          float sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float& x = s[j][2 * t + e];
-              x = ex2_approx(x - m_sub);
-              sum += x;
+            if (MASK) {
+              x[j].x = r + 8 * j + 2 * qp < lim[t] ? x[j].x : -INFINITY;
+              x[j].y = r + 8 * j + 2 * qp + 1 < lim[t] ? x[j].y : -INFINITY;
             }
-          l[t] = fmaf(l[t], alpha, sum);
-          scale_o[t] = alpha;
-          if constexpr (!QUANT) {
+            mx = fmaxf(mx, fmaxf(x[j].x, x[j].y));
+          }
+          bool moved = false;
+          float f = 1.f;
+          if (__any_sync(0xffffffffu, mx > m[t] + 30.f)) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float m_new = fmaxf(m[t], mx);
+            f = m_new == -INFINITY ? 1.f : ex2_approx(m[t] - m_new);   // -infinity: nothing seen yet
+            m[t] = m_new;
+            l2[t] = make_float2(l2[t].x * f, l2[t].y * f);
+            oz2[t] = make_float2(oz2[t].x * f, oz2[t].y * f);
+            moved = true;
+          }
+          const float nm = m[t] == -INFINITY ? 0.f : -m[t];
+          float ta = 0.f;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-              const float e0 = s[j][2 * t], e1 = s[j][2 * t + 1];
-              phi[t][j] = pack_bf16x2(e0, e1);
-              plo[t][j] = pack_bf16x2(e0 - bf16_lo(phi[t][j]), e1 - bf16_hi(phi[t][j]));
-            }
-          } else {
-            float z = 0.f, ta = 0.f;
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float& x = s[j][2 * t + e];
-                uint32_t par = e ? vpar[j].y : vpar[j].x;
-                // a row that this query does not see may hold anything
-                if (MASK) par = r + 8 * j + 2 * qp + e < lim[t] ? par : 0u;
-                if constexpr (FMT == kFmtFp8) {
-                  x *= __uint_as_float(par);
-                } else {
-                  z = fmaf(x, bf16_hi(par), z);
-                  x *= bf16_lo(par);
-                }
-                ta = fmaxf(ta, x);
+          for (int j = 0; j < NJ; ++j) {
+            x[j] = fadd2(x[j], make_float2(nm, nm));
+            x[j].x = ex2_approx(x[j].x);
+            x[j].y = ex2_approx(x[j].y);
+            l2[t] = fadd2(l2[t], x[j]);
+            if constexpr (!QUANT) {
+              phi[t][j] = pack_bf16x2(x[j].x, x[j].y);
+              plo[t][j] = pack_bf16x2(x[j].x - bf16_lo(phi[t][j]), x[j].y - bf16_hi(phi[t][j]));
+            } else {
+              uint32_t p0 = vpar[j].x, p1 = vpar[j].y;
+              if (MASK) {            // a row that this query does not see may hold anything
+                p0 = r + 8 * j + 2 * qp < lim[t] ? p0 : 0u;
+                p1 = r + 8 * j + 2 * qp + 1 < lim[t] ? p1 : 0u;
               }
-            oz[t] = fmaf(oz[t], alpha, z);
-            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 1));
-            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 2));
-            top_a[t] = fmaxf(top_a[t] * alpha, ta);
-            const float lead = top_a[t] * F[t];
-            if (top_a[t] > 0.f && !(lead <= 4096.f && lead >= 0.25f)) {
-              const int e = static_cast<int>(__float_as_uint(top_a[t]) >> 23);
-              const float f = __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 253)) << 23);
-              scale_o[t] *= f / F[t];
-              F[t] = f;
+              if constexpr (FMT == kFmtFp8) {
+                x[j] = fmul2(x[j], make_float2(__uint_as_float(p0), __uint_as_float(p1)));
+              } else {
+                oz2[t] = ffma2(x[j], make_float2(bf16_hi(p0), bf16_hi(p1)), oz2[t]);
+                x[j] = fmul2(x[j], make_float2(bf16_lo(p0), bf16_lo(p1)));
+              }
+              ta = fmaxf(ta, fmaxf(x[j].x, x[j].y));
+            }
+          }
+          if constexpr (QUANT) {
+            if (moved || __any_sync(0xffffffffu, ta > top[t])) {
+              ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 1));
+              ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 2));
+              lead[t] = fmaxf(lead[t] * f, ta);
+              const float now = lead[t] * F[t];
+              if (lead[t] > 0.f && !(now <= 4096.f && now >= 0.25f)) {
+                const int e = static_cast<int>(__float_as_uint(lead[t]) >> 23);
+                const float fn = __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 253)) << 23);
+                f *= fn / F[t];
+                F[t] = fn;
+              }
+              top[t] = lead[t] > 0.f ? 4096.f / F[t] : 0.f;
               moved = true;
             }
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-              phi[t][j] = pack_f16x2(s[j][2 * t] * F[t], s[j][2 * t + 1] * F[t]);
+            for (int j = 0; j < NJ; ++j) {
+              x[j] = fmul2(x[j], make_float2(F[t], F[t]));
+              phi[t][j] = pack_f16x2(x[j].x, x[j].y);
+            }
           }
+          if (moved) rescale(t, f);
         }
       };
       if (r + BR > lim_all) softmax(std::true_type{});
       else softmax(std::false_type{});
-      if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const float a_lo = __shfl_sync(0xffffffffu, scale_o[t], 8 * qp);
-          const float a_hi = __shfl_sync(0xffffffffu, scale_o[t], 8 * qp + 4);
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            o[t][k][0] *= a_lo;
-            o[t][k][1] *= a_hi;
-            o[t][k][2] *= a_lo;
-            o[t][k][3] *= a_hi;
-          }
-        }
-      }
       // ---- O^T += V^T P^T, 16 cache rows at a time
 #pragma unroll
       for (int g = 0; g < BR / 16; ++g) {
@@ -511,8 +553,11 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
     __syncthreads();                     // every warp's ring is read: results go there
 
     // ---- this warp's result, relative to 2^m: o = sum p v
+    float l[NT], oz[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      l[t] = l2[t].x + l2[t].y;
+      oz[t] = oz2[t].x + oz2[t].y;
       l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
       l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
       if constexpr (QUANT) {

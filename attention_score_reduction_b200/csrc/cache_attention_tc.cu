@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
           tc_fence_after();
           if (out) pv(t, t, gv % STAGES, r == 0);
           if (log) qk(t, qt, gk % STAGES);
-          if (elect_one()) mbar_arrive(&turn[t ^ 1]);
+          if (elect_one()) umma_commit(&turn[t ^ 1]);
           __syncwarp();
           if (out) release(gv);
           if (log) release(gk);
