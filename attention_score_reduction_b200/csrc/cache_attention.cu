@@ -100,6 +100,7 @@ struct RowsCfg {
   static constexpr int CODES = BR * RB;
   static constexpr int SLOT = 2 * CODES + (QUANT ? 8 * BR : 0);
   static constexpr int RING = WARPS * SLOTS * SLOT;
+  static constexpr int PAD = 4;                           // an item's start and end in tiles of work
 };
 
 // 16-byte chunk of row r as it lies in shared memory: chunks of a row are exchanged so
@@ -170,13 +171,12 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
 
   for (int64_t p = p0; p < p1; ++w) {
     if (w != spot.item) it = attn_item(a.c, shape, w);
-    const int n_tiles = it.n_tiles;
     const int64_t at = w_at;
-    w_at += n_tiles;
-    if (n_tiles == 0) continue;
-    const int t0 = static_cast<int>(p - at);
-    const int t1 = static_cast<int>(min(static_cast<int64_t>(n_tiles), p1 - at));
-    p = at + t1;
+    if (it.span == 0) continue;
+    int t0, t1;
+    const bool any = line_tiles(it, shape, at, p, p1, t0, t1);
+    p = w_at += it.span;
+    if (!any) continue;
     const int r_end = min(t1 * kRowsTile, it.vis);
 
     // ---- batches of this warp: rows r0 + (warp + WARPS n) * BR
@@ -238,6 +238,35 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
         }
       }
     };
+    // ---- query fragments and per-row limits (rows quad and quad + 8 of the item)
+    uint32_t qa[KS][2 * NT];
+    float cq[NT];        // log2-domain logit = cq S (+ cz z_j for int4)
+    float cz[NT];
+    int lim[NT];
+    // the pairs of fragment columns 2 qp and 2 qp + 8 of every k-step, as bf16: requested
+    // before the copies, which would keep them waiting
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int row = it.row0 + quad + 8 * t;
+      const bool live = quad + 8 * t < it.rows;
+      const int tok = row / shape.G;
+      lim[t] = live ? seen_rows(it, tok) : 0;
+      const uint16_t* qr = static_cast<const uint16_t*>(a.q) + it.u * a.q_unit +
+                           (row - tok * shape.G) * a.q_head + tok * a.q_row;
+#pragma unroll
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        // int4, a word of codes: elements e0..e7
+        const int el = FMT == kFmtInt4 ? 128 * (ks / 8) + 32 * qp + 4 * (ks % 8)
+                       : FMT == kFmtBf16 ? 32 * (ks / 2) + 8 * qp
+                                         : 64 * (ks / 4) + 16 * qp + 4 * (ks & 3);
+        if (live) v = *reinterpret_cast<const uint4*>(qr + el);
+        qa[ks][2 * t] = v.x;
+        qa[ks][2 * t + 1] = v.y;
+        qa[ks + 1][2 * t] = v.z;
+        qa[ks + 1][2 * t + 1] = v.w;
+      }
+    }
     // the first batches: all their pages, then all their copies, on their way while Q is
     // prepared
     {
@@ -252,47 +281,34 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
       }
     }
 
-    // ---- query fragments and per-row limits (rows quad and quad + 8 of the item)
-    uint32_t qa[KS][2 * NT];
-    float cq[NT];        // log2-domain logit = cq S (+ cz z_j for int4)
-    float cz[NT];
-    int lim[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int row = it.row0 + quad + 8 * t;
-      const bool live = quad + 8 * t < it.rows;
-      const int tok = row / shape.G;
-      lim[t] = live ? seen_rows(it, tok) : 0;
-      const uint16_t* qr = static_cast<const uint16_t*>(a.q) + it.u * a.q_unit +
-                           (row - tok * shape.G) * a.q_head + tok * a.q_row;
-      // the pairs of fragment columns 2 qp and 2 qp + 8 of every k-step, as bf16
-      uint32_t top = 0;
+      uint32_t top_q = 0;
 #pragma unroll
       for (int ks = 0; ks < KS; ks += 2) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if constexpr (FMT == kFmtInt4) {
-          // a word of codes: elements e0..e7 -> (e0, e4), (e1, e5) then (e2, e6), (e3, e7)
-          if (live) v = *reinterpret_cast<const uint4*>(qr + 128 * (ks / 8) + 32 * qp + 4 * (ks % 8));
-          v = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
-                         __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-        } else {
-          const int el = FMT == kFmtBf16 ? 32 * (ks / 2) + 8 * qp : 64 * (ks / 4) + 16 * qp + 4 * (ks & 3);
-          if (live) v = *reinterpret_cast<const uint4*>(qr + el);
+        uint32_t(&w0)[2 * NT] = qa[ks];
+        uint32_t(&w1)[2 * NT] = qa[ks + 1];
+        if constexpr (FMT == kFmtInt4) {     // (e0, e4), (e1, e5) then (e2, e6), (e3, e7)
+          const uint4 v = make_uint4(w0[2 * t], w0[2 * t + 1], w1[2 * t], w1[2 * t + 1]);
+          w0[2 * t] = __byte_perm(v.x, v.z, 0x5410);
+          w0[2 * t + 1] = __byte_perm(v.x, v.z, 0x7632);
+          w1[2 * t] = __byte_perm(v.y, v.w, 0x5410);
+          w1[2 * t + 1] = __byte_perm(v.y, v.w, 0x7632);
         }
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if constexpr (QUANT) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          qa[ks + k / 2][2 * t + (k & 1)] = w[k];
-          if constexpr (QUANT) top = max(top, max((w[k] << 16) & 0x7fff0000u, w[k] & 0x7fff0000u));
+          for (int k = 0; k < 2; ++k)
+            top_q = max(top_q, max(max((w0[2 * t + k] << 16) & 0x7fff0000u, w0[2 * t + k] & 0x7fff0000u),
+                                   max((w1[2 * t + k] << 16) & 0x7fff0000u, w1[2 * t + k] & 0x7fff0000u)));
         }
       }
       cq[t] = c;
       cz[t] = 0.f;
       if constexpr (QUANT) {
         // fp16, the row's largest element lifted to [2^14, 2^15)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = static_cast<int>(top >> 23) - 127;       // -127 for zeros and subnormals
+        top_q = max(top_q, __shfl_xor_sync(0xffffffffu, top_q, 1));
+        top_q = max(top_q, __shfl_xor_sync(0xffffffffu, top_q, 2));
+        const int e = static_cast<int>(top_q >> 23) - 127;       // -127 for zeros and subnormals
         const float f = __uint_as_float(static_cast<uint32_t>(min(max(127 + 14 - e, 1), 254)) << 23);
         // int4: codes meet Q as fp16 subnormals c 2^-24, those of the odd pairs as 16 c 2^-24
         const float f1 = FMT == kFmtInt4 ? f * 0.0625f : f;
@@ -437,7 +453,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
             moved = true;
           }
           const float nm = m[t] == -INFINITY ? 0.f : -m[t];
-          float ta = 0.f;
+          [[maybe_unused]] float ta = 0.f;
 #pragma unroll
           for (int j = 0; j < NJ; ++j) {
             x[j] = fadd2(x[j], make_float2(nm, nm));
@@ -605,8 +621,8 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
             xo[warp][2 * qp + b + 8 * t][elem(k, e)] = o[t][k][e + b];
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == n_tiles;
-    const int64_t slot = line_slot(all, cta, n_cta, at);
+    const bool whole = t1 - t0 == it.n_tiles;
+    const int64_t slot = line_slot(all, cta, n_cta, at + shape.pad);
     for (int i = threadIdx.x; i < it.rows * (D / 8); i += THREADS) {
       const int row = i / (D / 8), e = (i % (D / 8)) * 8;
       float M = xm[0][row];
@@ -648,7 +664,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
 template <int FMT, int D, int NT>
 cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st, int* launches) {
   using Cfg = RowsCfg<FMT, D>;
-  const AttnShape shape = attn_shape(a.q_lens, a.n_q, a.G, 8 * NT, kRowsTile);
+  const AttnShape shape = attn_shape(a.q_lens, a.n_q, a.G, 8 * NT, kRowsTile, Cfg::PAD);
   const int64_t items = a.c.units * shape.blocks;
   const int ctas = rows_ctas(FMT, D, shape.block);
   float2* ml = static_cast<float2*>(a.ws);
@@ -662,7 +678,7 @@ cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st, int* launches) 
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   *launches += 2;
-  return launch_attn_merge(a, shape, items, ctas, ml, o, st);
+  return launch_attn_merge(a, shape, items, ctas, false, ml, o, st);
 }
 
 }  // namespace

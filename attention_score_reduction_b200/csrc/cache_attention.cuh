@@ -26,9 +26,10 @@ __device__ __forceinline__ void attn_store8(const CacheAttnArgs& a, const AttnSh
   }
 }
 
-inline AttnShape attn_shape(const int32_t* q_lens, int n_q, int G, int block, int tile) {
+inline AttnShape attn_shape(const int32_t* q_lens, int n_q, int G, int block, int tile, int pad) {
   const int64_t rows = static_cast<int64_t>(n_q) * G;
-  return AttnShape{q_lens, n_q, G, block, static_cast<int>((rows + block - 1) / block), tile};
+  return AttnShape{q_lens, n_q, G, block, static_cast<int>((rows + block - 1) / block), tile,
+                   pad};
 }
 
 // Workspace: (m, l) of two slots per CTA, then their o rows.
@@ -41,9 +42,11 @@ inline size_t attn_ws_bytes(int ctas, int block, int d) {
 
 // out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the CTAs of each item
 // that no CTA covered whole; zeros for items (and rows) that see nothing.  A
-// slot holds shape.block rows of (m, l), m in the log2 domain, and of o[d].
+// slot holds shape.block rows of (m, l), m in the log2 domain, and of o: [block][d], or
+// (cols) [d / 4][block][4].
 cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, int64_t items,
-                              int ctas, const float2* ml, const float* o, cudaStream_t st);
+                              int ctas, bool cols, const float2* ml, const float* o,
+                              cudaStream_t st);
 
 // Few query rows a unit: mma.sync, straight from global memory.
 int rows_ctas(int format, int d, int block);

@@ -60,45 +60,79 @@ __device__ __forceinline__ void put_row(const CacheAttnArgs& a, const AttnShape&
 // Which item a block joins does not depend on the results, so it is found before
 // the wait for the grid that computes them.  Blocks are one per item, or (many
 // items: few of them are split) one per cut between two CTAs, of which the first
-// inside an item serves it.  Items with few parts (a long chunk: two or three)
-// give a row to each warp; with many (one token: dozens) the warps of a block
-// share a row's parts, so that their loads are in flight together.
+// inside an item serves it.
+struct Split {
+  AttnItem it;
+  int64_t c0, slot0;      // the first CTA with a part of the item, and its slot
+  int parts;              // 0: not split, or another block's
+
+  // slot of part i: later CTAs begin with the item
+  __device__ __forceinline__ int64_t slot(int i) const { return i == 0 ? slot0 : 2 * (c0 + i); }
+};
+__device__ __forceinline__ Split find_split(const CacheAttnArgs& a, const AttnShape& shape,
+                                            int64_t items, int ctas, int by_item) {
+  __shared__ int64_t scratch[kMergeWarps];
+  __shared__ LineSpot spot_s;
+  bool split = false;
+  Line<kMergeThreads> t(a.c, shape, items, scratch, &spot_s);
+  const int64_t n = line_ctas(t.all, ctas);
+  LineSpot spot;
+  spot.at = 0;
+  spot.info.span = 0;
+  if (by_item) {
+    spot = t.of_item(blockIdx.x);
+    split = spot.info.span > 0;
+  } else if (blockIdx.x + 1 < n) {
+    const int64_t cut = line_cut(t.all, blockIdx.x + 1, n);
+    spot = t.find(cut);
+    // the first cut among the item's tiles
+    split = spot.at + shape.pad < cut && line_cut(t.all, blockIdx.x, n) <= spot.at + shape.pad;
+  }
+  Split r;
+  r.it = spot.info;
+  r.c0 = r.slot0 = 0;
+  r.parts = 0;
+  if (split) {
+    const int64_t first = spot.at + shape.pad;
+    r.c0 = line_cta(t.all, first, n);
+    r.slot0 = line_slot(t.all, r.c0, n, first);
+    r.parts = static_cast<int>(line_cta(t.all, first + r.it.n_tiles - 1, n) - r.c0) + 1;
+    if (r.parts < 2) r.parts = 0;
+  }
+  return r;
+}
+
+// Items that see nothing: zeros.
+template <int D>
+__device__ __forceinline__ void put_zeros(const CacheAttnArgs& a, const AttnShape& shape,
+                                          int64_t items) {
+  const RowPart<D> zero = {};
+  for (int64_t z = blockIdx.x; z < items; z += gridDim.x) {
+    const AttnItem iz = attn_item(a.c, shape, z);
+    if (iz.n_tiles == 0)
+      for (int row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); row < iz.rows;
+           row += gridDim.y * kMergeWarps)
+        put_row<D>(a, shape, iz, row, zero, 0.f);
+  }
+}
+
+// Parts of the few-rows kernel: a slot's o is [row][D].  Items with few parts give a row
+// to each warp; with many (one token: dozens) the warps of a block share a row's parts,
+// so that their loads are in flight together.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     cache_attn_merge(const CacheAttnArgs a, const AttnShape shape, int64_t items, int ctas,
                      int by_item, const float2* __restrict__ ml, const float* __restrict__ o) {
-  __shared__ int64_t scratch[kMergeWarps];
-  __shared__ LineSpot spot_s;
   __shared__ RowPart<D> acc_s[kMergeWarps][32];
   __shared__ float l_s[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  bool split = false;
-  int64_t c0 = 0, c1 = 0;                // CTAs with a part of the item, inclusive
-  Line<kMergeThreads> t(a.c, shape, items, scratch, &spot_s);
-  const int64_t n = line_ctas(t.all, ctas);
-  LineSpot spot;
-  if (by_item) {
-    spot = t.of_item(blockIdx.x);
-    split = spot.info.n_tiles > 0;
-  } else if (blockIdx.x + 1 < n) {
-    const int64_t cut = line_cut(t.all, blockIdx.x + 1, n);
-    spot = t.find(cut);
-    // the first cut inside the item
-    split = spot.at < cut && line_cut(t.all, blockIdx.x, n) <= spot.at;
-  }
-  const int64_t before = spot.at;
-  const AttnItem it = spot.info;
-  if (split) {
-    c0 = line_cta(t.all, before, n);
-    c1 = line_cta(t.all, before + it.n_tiles - 1, n);
-    split = c0 != c1;
-  }
+  const Split sp = find_split(a, shape, items, ctas, by_item);
+  const AttnItem& it = sp.it;
   cudaGridDependencySynchronize();       // the partial results are complete and visible
 
-  if (split) {
-    const int parts = static_cast<int>(c1 - c0) + 1;
-    const int64_t slot0 = line_slot(t.all, c0, n, before);     // later CTAs begin with the item
-    auto part = [&](int i) { return (i == 0 ? slot0 : 2 * (c0 + i)) * shape.block; };
+  if (sp.parts > 0) {
+    const int parts = sp.parts;
+    auto part = [&](int i) { return sp.slot(i) * shape.block; };
     if (parts <= kWarpSplits) {
       for (int row = blockIdx.y * kMergeWarps + warp; row < it.rows; row += gridDim.y * kMergeWarps) {
         const float2 x = lane < parts ? ml[part(lane) + row] : make_float2(-INFINITY, 0.f);
@@ -185,25 +219,90 @@ __global__ void __launch_bounds__(kMergeThreads)
       }
     }
   }
-  // items that see nothing: zeros
-  const RowPart<D> zero = {};
-  for (int64_t z = blockIdx.x; z < items; z += gridDim.x) {
-    const AttnItem iz = attn_item(a.c, shape, z);
-    if (iz.n_tiles == 0)
-      for (int row = blockIdx.y * kMergeWarps + warp; row < iz.rows; row += gridDim.y * kMergeWarps)
-        put_row<D>(a, shape, iz, row, zero, 0.f);
+  put_zeros<D>(a, shape, items);
+}
+
+// Parts of the tensor-memory kernel: a slot's o is [D / 4][block] of four elements, as its
+// threads (a query row each) can store it with whole lines; a warp joins 32 rows of eight
+// elements, all its loads whole lines too.  One pass over the parts, four at a time, with
+// a running maximum.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads)
+    cache_attn_merge_cols(const CacheAttnArgs a, const AttnShape shape, int64_t items, int ctas,
+                          int by_item, const float2* __restrict__ ml,
+                          const float4* __restrict__ o) {
+  constexpr int AHEAD = 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Split sp = find_split(a, shape, items, ctas, by_item);
+  const AttnItem& it = sp.it;
+  cudaGridDependencySynchronize();       // the partial results are complete and visible
+
+  const int tasks = sp.parts > 0 ? ((it.rows + 31) / 32) * (D / 8) : 0;
+  for (int task = blockIdx.y * kMergeWarps + warp; task < tasks; task += gridDim.y * kMergeWarps) {
+    const int chunk = task % (D / 8), row = task / (D / 8) * 32 + lane;   // elements 8 chunk ..
+    if (row >= it.rows) continue;
+    float M = -INFINITY, L = 0.f;
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+    for (int i0 = 0; i0 < sp.parts; i0 += AHEAD) {
+      float2 x[AHEAD];
+      float4 p[AHEAD], q[AHEAD];
+      float top = M;
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        x[k] = make_float2(-INFINITY, 0.f);
+        p[k] = q[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + k < sp.parts) {
+          const int64_t s = sp.slot(i0 + k);
+          x[k] = ml[s * shape.block + row];
+          const float4* part = o + (s * (D / 4) + 2 * chunk) * shape.block + row;
+          p[k] = part[0];
+          q[k] = part[shape.block];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) top = fmax_nan(top, x[k].x);
+      const float sub = top == -INFINITY ? 0.f : top;
+      const float f = exp2f(M - sub);
+      M = top;
+      L *= f;
+      u = make_float4(u.x * f, u.y * f, u.z * f, u.w * f);
+      v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const float w = exp2f(x[k].x - sub);
+        L = fmaf(x[k].y, w, L);
+        u.x = fmaf(p[k].x, w, u.x);
+        u.y = fmaf(p[k].y, w, u.y);
+        u.z = fmaf(p[k].z, w, u.z);
+        u.w = fmaf(p[k].w, w, u.w);
+        v.x = fmaf(q[k].x, w, v.x);
+        v.y = fmaf(q[k].y, w, v.y);
+        v.z = fmaf(q[k].z, w, v.z);
+        v.w = fmaf(q[k].w, w, v.w);
+      }
+    }
+    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+    float r[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = L == 0.f ? 0.f : r[i] * inv;
+    attn_store8(a, shape, it, row, 8 * chunk, r);
   }
+  put_zeros<D>(a, shape, items);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, int64_t items,
-                              int ctas, const float2* ml, const float* o, cudaStream_t st) {
-  // y: blocks that share an item's rows, a row or eight at a time
+                              int ctas, bool cols, const float2* ml, const float* o,
+                              cudaStream_t st) {
+  // y: blocks that share an item's rows.  Few-rows parts: a row a block where an item is
+  // likely to have many parts, else eight; otherwise eight tasks of 32 rows x 8 elements.
   const int by_item = items <= ctas;
   const int64_t x = by_item ? items : ctas;
-  const int64_t y = by_item ? std::min<int64_t>(shape.block, std::max<int64_t>(1, 148 * 8 / x))
-                            : 148 * 8 / x;
+  const int64_t rows = std::min<int64_t>(shape.block, static_cast<int64_t>(shape.n_q) * shape.G);
+  int64_t y = cols ? (rows + 31) / 32 * (a.c.d / 8) / kMergeWarps
+                   : (ctas > kWarpSplits * items ? rows : (rows + kMergeWarps - 1) / kMergeWarps);
+  y = std::max<int64_t>(1, std::min<int64_t>(y, 148 * 8 / x));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
   cfg.blockDim = dim3(kMergeThreads);
@@ -213,6 +312,13 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
+  if (cols) {
+    const float4* o4 = reinterpret_cast<const float4*>(o);
+    return a.c.d == 128 ? cudaLaunchKernelEx(&cfg, cache_attn_merge_cols<128>, a, shape, items, ctas,
+                                             by_item, ml, o4)
+                        : cudaLaunchKernelEx(&cfg, cache_attn_merge_cols<256>, a, shape, items, ctas,
+                                             by_item, ml, o4);
+  }
   return a.c.d == 128 ? cudaLaunchKernelEx(&cfg, cache_attn_merge<128>, a, shape, items, ctas,
                                            by_item, ml, o)
                       : cudaLaunchKernelEx(&cfg, cache_attn_merge<256>, a, shape, items, ctas,

@@ -72,6 +72,7 @@ struct TcaCfg {
   static constexpr int SPLIT = 2;       // warpgroups that share a block's columns
   static constexpr int HC = BN / SPLIT;                // columns of S per softmax thread
   static constexpr int SW = SPLIT * NB;                // softmax warpgroups: block, share of the columns
+  static constexpr int PAD = 3;                        // an item's start and end in tiles of work
   static constexpr int KB = D / 64;                    // 128-byte column blocks of a row
   static constexpr int STAGE = BN * D * 2;             // one K or V tile: 32 KB
   static constexpr int Q_BYTES = D == 128 ? NB * 128 * D * 2 : 0;
@@ -242,17 +243,17 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
     int64_t p = p0, at = w_first_at;
     for (int64_t w = w_first; p < p1; ++w) {
       const AttnItem it = attn_item(a.c, shape, w);
-      if (it.n_tiles == 0) continue;
-      const int t0 = static_cast<int>(p - at);
-      const int t1 = static_cast<int>(min(static_cast<int64_t>(it.n_tiles), p1 - at));
+      if (it.span == 0) continue;
+      const int64_t begin = at;
+      int t0, t1;
+      const bool any = line_tiles(it, shape, begin, p, p1, t0, t1);
+      p = at += it.span;
+      if (!any) continue;
       Piece pc;
       pc.r0 = t0 * BN;
       pc.end = min(t1 * BN, it.vis);
       pc.n = t1 - t0;
-      const bool whole = pc.n == it.n_tiles;
-      if (!f(it, pc, whole, line_slot(all, cta, n_cta, at))) return;
-      p = at + t1;
-      at += it.n_tiles;
+      if (!f(it, pc, pc.n == it.n_tiles, line_slot(all, cta, n_cta, begin + shape.pad))) return;
     }
   };
   auto two_blocks = [&](const AttnItem& it) { return Cfg::NB == 2 && it.rows > 128; };
@@ -932,10 +933,11 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
               attn_store8(a, shape, it, row, h + i, x);
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(o_out + (slot * Cfg::BLOCK + row) * D + h);
+            // by fours of elements, then rows: a warp's stores are whole lines
+            float4* dst = reinterpret_cast<float4*>(o_out) + (slot * (D / 4) + h / 4) * Cfg::BLOCK + row;
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              dst[i / 4] = make_float4(at(i), at(i + 1), at(i + 2), at(i + 3));
+              dst[i / 4 * Cfg::BLOCK] = make_float4(at(i), at(i + 1), at(i + 2), at(i + 3));
           }
         }
       }
@@ -1048,7 +1050,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
 template <int FMT, int D>
 cudaError_t launch_tc_fd(const CacheAttnArgs& a, cudaStream_t st, int* launches) {
   using Cfg = TcaCfg<FMT, D>;
-  const AttnShape shape = attn_shape(a.q_lens, a.n_q, a.G, Cfg::BLOCK, Cfg::BN);
+  const AttnShape shape = attn_shape(a.q_lens, a.n_q, a.G, Cfg::BLOCK, Cfg::BN, Cfg::PAD);
   const int64_t items = a.c.units * shape.blocks;
   float2* ml = static_cast<float2*>(a.ws);
   float* o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + attn_ml_bytes(kTcCtas, Cfg::BLOCK));
@@ -1077,7 +1079,7 @@ cudaError_t launch_tc_fd(const CacheAttnArgs& a, cudaStream_t st, int* launches)
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   *launches += 2;
-  return launch_attn_merge(a, shape, items, kTcCtas, ml, o, st);
+  return launch_attn_merge(a, shape, items, kTcCtas, true, ml, o, st);
 }
 
 }  // namespace

@@ -4,7 +4,9 @@
 // rows its last row can see.  Heads keep very different numbers of rows
 // after eviction, so the items' tiles are laid end to end on one line and every
 // CTA takes an equal piece of it, crossing items where it must (a fixed number of
-// splits per head would wait for the longest head).  Lengths live on the device;
+// splits per head would wait for the longest head).  Beginning an item takes time of
+// its own (its queries, its result), so on the line an item is `pad` places longer than
+// its tiles, and a CTA that crosses into one has that much less to do.  Lengths live on the device;
 // every CTA adds them up itself.  A CTA's part of an item that it does not cover
 // whole is a partial result; a CTA has at most two, of its first and its last
 // item, in slots 2 cta and 2 cta + 1.
@@ -23,6 +25,7 @@ struct AttnShape {
   int block;       // query rows of one item; row r of a unit is token r / G, head r % G
   int blocks;      // items per unit
   int tile;        // cache rows of one tile
+  int pad;         // places on the line before an item's first tile
 };
 
 struct AttnItem {
@@ -32,6 +35,7 @@ struct AttnItem {
   int row0, rows;  // query rows [row0, row0 + rows)
   int vis;         // cache rows the item's last query row sees
   int n_tiles;
+  int span;        // places on the line
 };
 
 // Cache rows that token i sees (may be negative: none).
@@ -48,12 +52,13 @@ __device__ __forceinline__ AttnItem attn_item(const CacheArgs& c, const AttnShap
   it.vis = 0;
   if (it.rows > 0) it.vis = max(0, seen_rows(it, (it.row0 + it.rows - 1) / s.G));
   it.n_tiles = (it.vis + s.tile - 1) / s.tile;
+  it.span = it.n_tiles > 0 ? it.n_tiles + s.pad : 0;
   return it;
 }
 
 // An item as the thread that counted its tiles hands it to the block.
 struct LineSpot {
-  int64_t item, at;      // the item and the place of its first tile
+  int64_t item, at;      // the item and its first place
   AttnItem info;
 };
 
@@ -67,8 +72,8 @@ struct Line {
   int64_t items;
   int64_t* sums;
   LineSpot* spot;
-  int64_t all;         // tiles of all items
-  int64_t mine_end;    // items <= THREADS: tiles up to and with item threadIdx.x
+  int64_t all;         // places of all items
+  int64_t mine_end;    // items <= THREADS: places up to and with item threadIdx.x
   AttnItem mine;
 
   __device__ Line(const CacheArgs& c_, const AttnShape& s_, int64_t items_, int64_t* sums_,
@@ -78,11 +83,11 @@ struct Line {
     if (items <= THREADS) {
       if (threadIdx.x < items) {
         mine = attn_item(c, s, threadIdx.x);
-        v = mine.n_tiles;
+        v = mine.span;
       }
       mine_end = scan(v, &all);
     } else {
-      for (int64_t i = threadIdx.x; i < items; i += THREADS) v += attn_item(c, s, i).n_tiles;
+      for (int64_t i = threadIdx.x; i < items; i += THREADS) v += attn_item(c, s, i).span;
       scan(v, &all);
     }
   }
@@ -108,22 +113,22 @@ struct Line {
     return v;
   }
 
-  // The spot of tile p (0 <= p < all); one use per block.
+  // The spot of place p (0 <= p < all); one use per block.
   __device__ LineSpot find(int64_t p) {
     if (items <= THREADS) {
-      if (threadIdx.x < items && mine_end - mine.n_tiles <= p && p < mine_end)
-        *spot = LineSpot{static_cast<int64_t>(threadIdx.x), mine_end - mine.n_tiles, mine};
+      if (threadIdx.x < items && mine_end - mine.span <= p && p < mine_end)
+        *spot = LineSpot{static_cast<int64_t>(threadIdx.x), mine_end - mine.span, mine};
     } else {
       int64_t base = 0;
       for (int64_t i0 = 0; i0 < items; i0 += THREADS) {
         const int64_t i = i0 + threadIdx.x;
         AttnItem it;
-        it.n_tiles = 0;
+        it.span = 0;
         if (i < items) it = attn_item(c, s, i);
         int64_t sum;
         __syncthreads();
-        const int64_t end = base + scan(it.n_tiles, &sum);
-        if (end - it.n_tiles <= p && p < end) *spot = LineSpot{i, end - it.n_tiles, it};
+        const int64_t end = base + scan(it.span, &sum);
+        if (end - it.span <= p && p < end) *spot = LineSpot{i, end - it.span, it};
         base += sum;
         if (base > p) break;      // the same for every thread
       }
@@ -135,10 +140,10 @@ struct Line {
   // The spot of item w; one use per block.
   __device__ LineSpot of_item(int64_t w) {
     if (items <= THREADS) {
-      if (threadIdx.x == w) *spot = LineSpot{w, mine_end - mine.n_tiles, mine};
+      if (threadIdx.x == w) *spot = LineSpot{w, mine_end - mine.span, mine};
     } else {
       int64_t v = 0, sum;
-      for (int64_t i = threadIdx.x; i < w; i += THREADS) v += attn_item(c, s, i).n_tiles;
+      for (int64_t i = threadIdx.x; i < w; i += THREADS) v += attn_item(c, s, i).span;
       __syncthreads();
       scan(v, &sum);
       if (threadIdx.x == 0) *spot = LineSpot{w, sum, attn_item(c, s, w)};
@@ -148,8 +153,18 @@ struct Line {
   }
 };
 
-// CTAs with work: no more than there are tiles, so that every one's piece holds
-// at least one tile and every slot between an item's first and last CTA is written.
+// The tiles [t0, t1) of an item that begins at place `at` within places [p, p1); false
+// if there are none.
+__device__ __forceinline__ bool line_tiles(const AttnItem& it, const AttnShape& s, int64_t at,
+                                           int64_t p, int64_t p1, int& t0, int& t1) {
+  const int64_t first = at + s.pad;
+  t0 = static_cast<int>(max(p - first, static_cast<int64_t>(0)));
+  t1 = static_cast<int>(max(min(p1 - first, static_cast<int64_t>(it.n_tiles)), static_cast<int64_t>(0)));
+  return t0 < t1;
+}
+
+// CTAs of the line: no more than there are places, so that no piece is empty and every
+// CTA between those with an item's first and last tile has tiles of it, and a slot.
 __device__ __forceinline__ int64_t line_ctas(int64_t all, int64_t grid) {
   return all < grid ? all : grid;
 }
@@ -163,11 +178,11 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 __device__ __forceinline__ int64_t line_cut(int64_t all, int64_t i, int64_t n) {
   return quotient(all * i, n);
 }
-// Slot of CTA i's part of the item whose tiles begin at `before` on the line.
-__device__ __forceinline__ int64_t line_slot(int64_t all, int64_t i, int64_t n, int64_t before) {
-  return 2 * i + (line_cut(all, i, n) >= before ? 0 : 1);
+// Slot of CTA i's part of the item whose first tile is at place `first`.
+__device__ __forceinline__ int64_t line_slot(int64_t all, int64_t i, int64_t n, int64_t first) {
+  return 2 * i + (line_cut(all, i, n) >= first ? 0 : 1);
 }
-// The CTA that takes tile p.
+// The CTA that takes place p.
 __device__ __forceinline__ int64_t line_cta(int64_t all, int64_t p, int64_t n) {
   int64_t i = quotient(p * n, all);
   while (i + 1 < n && line_cut(all, i + 1, n) <= p) ++i;
