@@ -69,9 +69,8 @@ struct TcaCfg {
   static constexpr int BN = D == 128 ? 128 : 64;       // cache rows of a tile
   static constexpr int NB = D == 128 ? 2 : 1;          // blocks of 128 query rows
   static constexpr int BLOCK = 128 * NB;               // query rows of an item
-  static constexpr int SPLIT = 2;       // warpgroups that share a block's columns
-  static constexpr int HC = BN / SPLIT;                // columns of S per softmax thread
-  static constexpr int SW = SPLIT * NB;                // softmax warpgroups: block, share of the columns
+  static constexpr int HC = BN / 2;                    // columns of S per softmax thread
+  static constexpr int SW = 2 * NB;                    // softmax warpgroups: block, half of the columns
   static constexpr int PAD = 3;                        // an item's start and end in tiles of work
   static constexpr int KB = D / 64;                    // 128-byte column blocks of a row
   static constexpr int STAGE = BN * D * 2;             // one K or V tile: 32 KB
@@ -96,8 +95,9 @@ struct TcaCfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = Q_BYTES;
   static constexpr int OFF_RAW = OFF_KV + STAGES * STAGE;
-  // what the unpacking tells the softmax: per V tile e of each row, then 2^-e; per K
-  // tile the powers of two of its pieces.  Rings, long enough for how far the
+  // what the unpacking tells the softmax: per V tile e of its pieces (64 rows) or, where
+  // a piece's rows differ too much, e of each row, then 2^-e; per K tile the powers of
+  // two of its pieces.  Rings, long enough for how far the
   // parameters can be ahead of the softmax: the softmax of tile j precedes the
   // release of V tile j, so at most STAGES + RAW_SLOTS (+ 1) tiles of K and V follow
   static constexpr int V_RING = 6, K_RING = 8;
@@ -105,7 +105,8 @@ struct TcaCfg {
   static constexpr int OFF_KSCALE = OFF_ROWEXP + (QUANT ? V_RING * BN * 8 : 0);
   static_assert(!QUANT || (STAGES + RAW_SLOTS * 64 / BN + 1) / 2 + 1 <= V_RING, "ring of row powers");
   static_assert(!QUANT || (STAGES + RAW_SLOTS * 64 / BN + 1) / 2 + 2 <= K_RING, "ring of K powers");
-  static constexpr int OFF_LIFT = OFF_KSCALE + (QUANT ? K_RING * 8 : 0);   // scale of each Q row
+  static constexpr int OFF_VSCALE = OFF_KSCALE + (QUANT ? K_RING * 8 : 0);
+  static constexpr int OFF_LIFT = OFF_VSCALE + (QUANT ? V_RING * 8 : 0);   // scale of each Q row
   static constexpr int OFF_XCH = OFF_LIFT + (QUANT ? 256 * 4 : 0);       // a float per row
   // (m, l) per row and warpgroup at an item's end: d = 128 where Q was, else its own
   static constexpr int OFF_ML = D == 128 ? OFF_Q : OFF_XCH + BLOCK * 4;
@@ -124,10 +125,16 @@ struct TcaCfg {
   static constexpr int R_CTL = R_LAUNCH == 0 ? 0 : 40;
   static constexpr int R_SOFT = R_LAUNCH == 0 ? 0 : 88;
   static constexpr int R_UNPACK = R_LAUNCH == 0 ? 0 : 88;
-  static_assert(R_CTL + SW * R_SOFT + R_UNPACK <= R_LAUNCH * THREADS / 128 || R_LAUNCH == 0, "register split");
+  static_assert(R_CTL + SW * R_SOFT + UW * R_UNPACK <= R_LAUNCH * THREADS / 128 || R_LAUNCH == 0, "register split");
   static constexpr int CH = 32;                        // columns a thread takes at a time
-  static constexpr bool HOLD = HC == CH;               // and keeps from the maximum to the exponentials
-  static constexpr int POLY = 2;     // of 8 pairs of exponentials, those on the FMA pipe
+  // and keeps from the maximum to the exponentials (quantised: kept, others spill)
+  static constexpr bool HOLD = HC == CH && !QUANT;
+  // quantised: one power of two for 64 rows of V where it will do, instead of one a row.
+  // d = 128: a seventh faster; d = 256: as fast with either, the plainer one
+  static constexpr bool ONE_E = QUANT && D == 128;
+  // of 8 pairs of exponentials, those on the FMA pipe (beside the unpacking at d = 128,
+  // issue slots are scarcer)
+  static constexpr int POLY = ONE_E ? 0 : 2;
 };
 
 // Shared-memory matrix descriptors under the 128-byte swizzle, low words (the high
@@ -212,9 +219,9 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128 * Cfg::SPLIT);
+      mbar_init(&p_full[i], 256);
       mbar_init(&o_full[i], 1);
-      mbar_init(&q_full[i], 128 * Cfg::SPLIT);
+      mbar_init(&q_full[i], 256);
       mbar_init(&turn[i], 1);
     }
     mbar_init(&pv_done[0], 1);
@@ -543,9 +550,29 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   zero[k] = top == 0.f;
                   e[k] = nan[k] ? -110 : max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
                 }
-                // V: not below 2^-60 (nor for zeros), where 2^(x' - m) would underflow
-                // beside other rows
-                ev[k] = nan[k] || zero[k] ? 0 : max(e[k], -60);
+                // V: within 2^+-50, so that 2^(x' - m) of no row underflows beside another's
+                // that matters no more; fp16 holds what is beyond, up to 2^64
+                ev[k] = nan[k] || zero[k] ? 0 : min(max(e[k], -50), 50);
+              }
+              // V: one power of two for the 64 rows, too, if none is 2^8 below the largest
+              // (their products with it are exact, or as good as their own)
+              bool own_e = is_v && !Cfg::ONE_E;
+              if (Cfg::ONE_E && is_v) {
+                int hi = -1000, lo = 1000;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                  if (!zero[k]) {
+                    hi = max(hi, ev[k]);
+                    lo = min(lo, nan[k] ? -1000 : ev[k]);
+                  }
+                hi = __reduce_max_sync(0xffffffffu, hi);
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                own_e = hi - lo > 8;
+                if (hi == -1000) hi = 0;
+                if (!own_e) ev[0] = ev[1] = hi;
+                if (lane == 0)
+                  reinterpret_cast<float*>(smem + Cfg::OFF_VSCALE)[2 * (v_tile % Cfg::V_RING) + h / 64] =
+                      own_e ? INFINITY : static_cast<float>(hi);
               }
               // K: one power of two for the 64 rows, the largest
               const int top_e = __reduce_max_sync(0xffffffffu, max(e[0], e[1]));
@@ -567,7 +594,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   mul = nan[k] ? 0x7e007e00u : pack_f16x2(bf16_lo(par[k]) * f, bf16_hi(par[k]) * f);
                 }
                 params[lane + 32 * k] = mul;
-                if (is_v) {
+                if (own_e) {
                   row_e[lane + 32 * k] = nan[k] ? NAN : static_cast<float>(ev[k]);
                   row_e[BN + lane + 32 * k] = __uint_as_float(static_cast<uint32_t>(127 - ev[k]) << 23);
                 }
@@ -593,7 +620,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
     constexpr int HC = Cfg::HC, CH = Cfg::CH;
     constexpr int kAll = 128 * Cfg::SW;
     const int sw = (warp - Cfg::SOFT_WARP0) >> 2;
-    const int t = sw / Cfg::SPLIT, half = sw % Cfg::SPLIT;
+    const int t = sw >> 1, half = sw & 1;
     const int quarter = warp & 3;
     const int lrow = quarter * 32 + lane;                 // TMEM lane = row of the 128-row block
     const int pair_bar = 2 + t * 4 + quarter;              // the two warps with the same rows
@@ -689,23 +716,21 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
         // each half of the columns of the row's TMEM lane
         const int r = it.row0 + row, tok = r / shape.G, head = r - tok * shape.G;
         const uint4* src = reinterpret_cast<const uint4*>(qu + head * a.q_head + tok * a.q_row) +
-                           half * (D / (8 * Cfg::SPLIT));
+                           half * (D / 16);
         float f = 1.f;
         if constexpr (Cfg::QUANT) {
           uint32_t top = 0;
 #pragma unroll
-          for (int i = 0; i < D / (8 * Cfg::SPLIT); ++i)
+          for (int i = 0; i < D / 16; ++i)
             top = max(top, magnitude(live ? src[i] : make_uint4(0, 0, 0, 0)));
-          if constexpr (Cfg::SPLIT == 2) {
-            lifts[half * 128 + lrow] = __uint_as_float(top);
-            named_barrier_sync(1, kAll);
-            top = max(top, __float_as_uint(lifts[(half ^ 1) * 128 + lrow]));
-          }
+          lifts[half * 128 + lrow] = __uint_as_float(top);
+          named_barrier_sync(1, kAll);
+          top = max(top, __float_as_uint(lifts[(half ^ 1) * 128 + lrow]));
           f = lift_of(top);
           cq = c / f;
         }
 #pragma unroll
-        for (int h = 0; h < D / (64 * Cfg::SPLIT); ++h) {
+        for (int h = 0; h < D / 128; ++h) {
           uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -715,7 +740,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
             v[4 * i + 2] = x.z;
             v[4 * i + 3] = x.w;
           }
-          tmem_st32_async(lane_base + Cfg::Q0 + half * (D / (2 * Cfg::SPLIT)) + 32 * h, v);
+          tmem_st32_async(lane_base + Cfg::Q0 + half * (D / 4) + 32 * h, v);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -733,22 +758,27 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
         const int col0 = pc.r0 + j * BN + half * HC;
         const bool masked = pc.r0 + j * BN + BN > lim_all;
         const float* row_e = nullptr;        // e of these V rows; 2^-e are BN floats on
-        const float* ks = nullptr;           // powers of two of their K pieces
+        float ce = c, e_all = 0.f;           // x (x') = ce S + e; e_all: e of all of them, or infinity
         if constexpr (Cfg::QUANT) {
           const uint32_t gv = 2 * n_tile + min(j + (two ? 1 : 2), pc.n) + j;
           const int sv = gv % STAGES;
           ok = ok && wait_warp(&kv_full[sv], (gv / STAGES) & 1, ctl);
           row_e = reinterpret_cast<const float*>(smem + Cfg::OFF_ROWEXP) +
                   ((n_tile + j) % Cfg::V_RING) * (2 * BN) + half * HC;
-          ks = reinterpret_cast<const float*>(smem + Cfg::OFF_KSCALE) +
-               2 * ((n_tile + j) % Cfg::K_RING) + (half * HC) / 64;
+          // this half's columns are of one piece; never 0, which would turn -infinity to NaN
+          ce = fmaxf(cq * reinterpret_cast<const float*>(smem + Cfg::OFF_KSCALE)[
+                         2 * ((n_tile + j) % Cfg::K_RING) + (half * HC) / 64], 1.17549435e-38f);
+          if constexpr (Cfg::ONE_E)
+            e_all = reinterpret_cast<const float*>(smem + Cfg::OFF_VSCALE)[
+                2 * ((n_tile + j) % Cfg::V_RING) + (half * HC) / 64];
         }
+        const bool own_e = Cfg::QUANT && (!Cfg::ONE_E || e_all == INFINITY);
         tc_fence_after();
-        // CH columns: S (bf16), or x' = x + e; -infinity where this row does not see
+        // CH columns: S or, if each row has its own e, x' = x + e; -infinity where this row
+        // does not see
         auto load = [&](int h, float (&v)[CH]) {
           tmem_ld_tile(s_addr + h, v);
-          if constexpr (Cfg::QUANT) {
-            const float ce = cq * ks[h / 64];          // x = ce S
+          if (Cfg::QUANT && own_e) {
             const float2 ce2 = make_float2(ce, ce);
 #pragma unroll
             for (int i = 0; i < CH; i += 4) {
@@ -769,7 +799,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
         };
         // columns that are not held are read again for the exponentials
         float s_row[Cfg::HOLD ? HC / CH : 1][CH];
-        float mx[4] = {m, m, m, m};
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         if (ok) {
 #pragma unroll
           for (int h = 0; h < HC / CH; ++h) {
@@ -782,25 +812,20 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
           }
         }
         float cand = fmax_nan(fmax_nan(mx[0], mx[1]), fmax_nan(mx[2], mx[3]));
+        if (Cfg::QUANT && !own_e) cand = fmaf(cand, ce, e_all);
+        cand = fmax_nan(m, cand);
         bool need = !(cand - m <= lazy) && cand != -INFINITY;
-        if constexpr (Cfg::SPLIT == 2) {
-          // both warps of these rows have to move together (or to give up together)
-          need = named_barrier_or(pair_bar, 64, need || !ok);
-          if (need) {
-            if (half == 0) *xch = cand;
-            if (named_barrier_or(pair_bar, 64, !ok)) { ok = false; break; }
-            if (half == 1) {
-              cand = fmax_nan(cand, *xch);
-              *xch = cand;
-            }
-            named_barrier_sync(pair_bar, 64);
-            if (half == 0) cand = *xch;
-          }
-        } else {
-          if (!ok) break;
-          need = __any_sync(0xffffffffu, need);
-        }
+        // both warps of these rows have to move together (or to give up together)
+        need = named_barrier_or(pair_bar, 64, need || !ok);
         if (need) {
+          if (half == 0) *xch = cand;
+          if (named_barrier_or(pair_bar, 64, !ok)) { ok = false; break; }
+          if (half == 1) {
+            cand = fmax_nan(cand, *xch);
+            *xch = cand;
+          }
+          named_barrier_sync(pair_bar, 64);
+          if (half == 0) cand = *xch;
           const float f = cand == -INFINITY ? 1.f : ex2_approx(Cfg::QUANT ? m - cand : (m - cand) * c);
           if (j != j0) {
             // d = 256: S was ready before the last O; wait for that product
@@ -809,27 +834,30 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                              ((j & 1 ? n_even : n_odd) + ((j - 1) >> 1)) & 1, ctl);
             tc_fence_after();
 #pragma unroll 1
-            for (int h = 0; h < D / Cfg::SPLIT; h += 32) {
+            for (int h = 0; h < D / 2; h += 32) {
               float o[32];
-              tmem_ld32(o_addr + half * (D / Cfg::SPLIT) + h, o);
+              tmem_ld32(o_addr + half * (D / 2) + h, o);
               uint32_t u[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-              tmem_st32_async(o_addr + half * (D / Cfg::SPLIT) + h, u);
+              tmem_st32_async(o_addr + half * (D / 2) + h, u);
             }
             tmem_wait_st();
           }
           l *= f;
           m = cand;
         }
-        const float nb = m == -INFINITY ? 0.f : (Cfg::QUANT ? -m : -m * c);
-        const float2 c2 = make_float2(c, c), nb2 = make_float2(nb, nb);
+        float nb = m == -INFINITY ? 0.f : (Cfg::QUANT ? -m : -m * c);
+        if (Cfg::QUANT && !own_e) nb += e_all;
+        const float2 ce2 = make_float2(ce, ce), nb2 = make_float2(nb, nb);
         float2 acc[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) acc[q] = make_float2(0.f, 0.f);
         // POLY of eight pairs go to the FMA pipe, where nothing is masked (the polynomial
         // has no 2^-infinity)
-        auto weights = [&](auto poly) {
+        auto weights = [&](auto poly, auto own) {
+          constexpr bool OWN = decltype(own)::value;
+          constexpr int POLY = decltype(poly)::value;
 #pragma unroll
           for (int hh = 0; hh < HC / CH; ++hh) {
             const int h = hh * CH;
@@ -841,32 +869,41 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
 #pragma unroll
               for (int q = 0; q < 8; ++q) {
                 const int e0 = i + 2 * q;
-                const float2 x = Cfg::QUANT ? fadd2(make_float2(v[e0], v[e0 + 1]), nb2)
-                                            : ffma2(make_float2(v[e0], v[e0 + 1]), c2, nb2);
+                const float2 x = OWN ? fadd2(make_float2(v[e0], v[e0 + 1]), nb2)
+                                                      : ffma2(make_float2(v[e0], v[e0 + 1]), ce2, nb2);
                 float2 e;
-                if (q < decltype(poly)::value) {
+                if (q < POLY) {
                   e = exp2_poly2(x);
                 } else {
                   e.x = ex2_approx(x.x);
                   e.y = ex2_approx(x.y);
                 }
-                if constexpr (Cfg::QUANT) {
-                  const float2 inv = *reinterpret_cast<const float2*>(row_e + BN + h + e0);
-                  acc[q & 3] = ffma2(e, inv, acc[q & 3]);
-                  pk[e0 / 2] = pack_f16x2(e.x, e.y);
-                } else {
+                if constexpr (OWN)
+                  acc[q & 3] = ffma2(e, *reinterpret_cast<const float2*>(row_e + BN + h + e0), acc[q & 3]);
+                else
                   acc[q & 3] = fadd2(acc[q & 3], e);
-                  pk[e0 / 2] = pack_bf16x2(e.x, e.y);
-                }
+                pk[e0 / 2] = Cfg::QUANT ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
               }
             // over columns of this half's S that are read
             tmem_st_tile(s_addr + h / 2, pk);
           }
         };
-        if (masked) weights(std::integral_constant<int, 0>{});
-        else weights(std::integral_constant<int, Cfg::POLY>{});
+        using none = std::integral_constant<int, 0>;
+        using poly = std::integral_constant<int, Cfg::POLY>;
+        constexpr auto own = std::integral_constant<bool, Cfg::QUANT>{};      // e of each row, if any
+        if (Cfg::ONE_E && !own_e) {
+          if (masked) weights(none{}, std::false_type{});
+          else weights(poly{}, std::false_type{});
+        } else if (masked || Cfg::ONE_E) {
+          weights(none{}, own);
+        } else {
+          weights(poly{}, own);
+        }
         const float2 sum = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-        l += sum.x + sum.y;
+        if (Cfg::QUANT && !own_e)      // of 2^x, not 2^x'
+          l = fmaf(sum.x + sum.y, __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(e_all)) << 23), l);
+        else
+          l += sum.x + sum.y;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&p_full[b]);
@@ -887,14 +924,12 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
       // one view of the abort flag, and (m, l) are visible
       if (named_barrier_or(1, kAll, !ok || *abort_flag != 0)) return false;
       float f0 = 1.f, f1 = 0.f, M = m2;
-      auto block_l = [&](int blk) {             // a row's sum over its share of the columns
-        float v = mls[blk * Cfg::SPLIT * 128 + lrow].y;
-        if constexpr (Cfg::SPLIT == 2) v += mls[(blk * 2 + 1) * 128 + lrow].y;
-        return v;
+      auto block_l = [&](int blk) {             // a row's sum over both halves of the columns
+        return mls[blk * 256 + lrow].y + mls[blk * 256 + 128 + lrow].y;
       };
       float L = block_l(0);
       if (join) {
-        const float2 x = mls[lrow], y = mls[Cfg::SPLIT * 128 + lrow];
+        const float2 x = mls[lrow], y = mls[256 + lrow];
         M = fmax_nan(x.x, y.x);
         const float sub = M == -INFINITY ? 0.f : M;
         f0 = ex2_approx(x.x - sub);
@@ -902,7 +937,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
         L = L * f0 + block_l(1) * f1;
       }
       // every group writes its share of the elements
-      const int share = D / (join ? Cfg::SW : Cfg::SPLIT);
+      const int share = D / (join ? Cfg::SW : 2);
       const int h0 = (join ? sw : half) * share, h1 = h0 + share;
       const uint32_t oa = lane_base + Cfg::O0 + (join ? 0 : t * D);
       const float inv = !whole ? 1.f : (L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN));

@@ -475,6 +475,23 @@ def test_magnitudes(kc, fmt, d, n_q):
     check_attention(c, q, c.attend(q, out_dtype=torch.float32), lens, [n_q])
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("n_q", [1, 40])
+@pytest.mark.parametrize("stride", [1, 97])
+def test_value_rows_far_apart(kc, fmt, d, n_q, stride):
+    """Value rows from 2^-46 to 2^46, neighbours alike or far apart: the sum of the
+    weights counts the small ones as well."""
+    lens = [600]
+    c = make_cache(kc, fmt, [0], d, 32, 600)
+    k, v = rows_bf16(95, 1, 600, d), rows_bf16(96, 1, 600, d)
+    exps = torch.linspace(-46, 46, 600)[(torch.arange(600) * stride) % 600]
+    v = (v.float() * torch.exp2(exps).view(1, -1, 1)).to(torch.bfloat16)
+    c.write(k.cuda(), v.cuda())
+    q = rows_bf16(97, 1, 3, n_q, d).cuda()
+    check_attention(c, q, c.attend(q, out_dtype=torch.float32), lens, [n_q])
+
+
 @pytest.mark.parametrize("n_q", [1, 20])
 @pytest.mark.parametrize("fmt", FMTS)
 def test_non_finite_rows_reach_who_sees_them(kc, fmt, n_q):
