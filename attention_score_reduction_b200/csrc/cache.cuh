@@ -47,6 +47,16 @@ __device__ __forceinline__ int64_t cache_slot(const CacheArgs& c, int64_t u, int
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// none of eight bf16 is infinite or NaN
+__device__ __forceinline__ bool bf16x8_finite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool ok = true;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    ok = ok && (w[k] & 0x7f80u) != 0x7f80u && (w[k] & 0x7f800000u) != 0x7f800000u;
+  return ok;
+}
+
 // two floats as bf16x2 (x in the low half), round to nearest even
 __device__ __forceinline__ uint32_t pack_bf16x2(float x, float y) {
   uint32_t r;

@@ -33,6 +33,7 @@
 // two bf16 parts (about 16 bits).
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -372,6 +373,24 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
       n_slot = n_slot + 1 == Cfg::SLOTS ? 0 : n_slot + 1;
       copies_wait<Cfg::SLOTS - 1>();
       __syncwarp();
+      if constexpr (!QUANT) {
+        // the chunk's own tokens, which not every query row sees, must not reach those as
+        // 0 * NaN: what is not finite becomes zero, and rows that see it NaN
+        if (lim_all < min(r + BR, r_end)) {
+          int bad = INT_MAX;
+          for (int i = lane; i < Cfg::CODES / 16; i += 32) {
+            const int row = r + i / (RB / 16);
+            const uint32_t at = slot + Cfg::CODES + 16 * i;
+            if (row < lim_all || row >= r_end || bf16x8_finite(lds16(at))) continue;
+            bad = min(bad, row);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+          }
+          bad = __reduce_min_sync(0xffffffffu, bad);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (bad < lim[t]) l2[t].x = NAN;
+        }
+      }
       // ---- products of the logits
       float s[NJ][4];
 #pragma unroll

@@ -116,7 +116,7 @@ struct TcaCfg {
   // raw_empty[RAW_SLOTS]
   static constexpr int N_BARS = 3 * STAGES + 13 + 3 * RAW_SLOTS;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
-  static constexpr int BYTES = OFF_MISC + 16;
+  static constexpr int BYTES = OFF_MISC + 32;          // TMEM address, abort flag, bad rows of four items
   static constexpr int SMEM = BYTES + 1024;
   static_assert(SMEM <= 232448 - 256, "exceeds 227 KB of shared memory with the static part");
   // registers a thread of each warpgroup after the split (0: no split); the sums
@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
   uint64_t* raw_empty = raw_ready + Cfg::RAW_SLOTS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::OFF_MISC + 4);
+  int* bad_row = reinterpret_cast<int*>(smem + Cfg::OFF_MISC + 16);   // see the end of a bf16 item
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int64_t cta = blockIdx.x;
 
@@ -264,6 +265,10 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
     }
   };
   auto two_blocks = [&](const AttnItem& it) { return Cfg::NB == 2 && it.rows > 128; };
+  // Rows of the piece that all query rows of the item see; tiles that go further are ragged.
+  auto seen_by_all = [&](const AttnItem& it, const Piece& pc) {
+    return min(seen_rows(it, it.row0 / shape.G), pc.end);
+  };
   // K and V tiles in the order the MMAs use them: f(is_v, tile).  V tile j comes
   // after min(j + ahead, n) K tiles and j V tiles.
   auto each_stage = [&](const AttnItem& it, const Piece& pc, auto&& f) -> bool {
@@ -288,6 +293,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
       uint32_t g = 0;
       if (a.test_stall == 0)
         each_item([&](const AttnItem& it, const Piece& pc, bool, int64_t) {
+          const int all_see = seen_by_all(it, pc);
           return each_stage(it, pc, [&](bool is_v, int j) {
             const int s = g % STAGES;
             const int r = pc.r0 + j * BN + lane * box;       // lane i brings page box i
@@ -299,8 +305,8 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
             }
             const int n_box = __popc(__ballot_sync(0xffffffffu, mine));
             if (!wait_warp(&kv_empty[s], ((g / STAGES) & 1) ^ 1, ctl)) return false;
-            // the last V tile goes by way of warp 3
-            uint64_t* full = is_v && pc.end - (pc.r0 + j * BN) < BN ? &tail_full[s] : &kv_full[s];
+            // the last V tiles go by way of warp 3
+            uint64_t* full = is_v && pc.r0 + (j + 1) * BN > all_see ? &tail_full[s] : &kv_full[s];
             if (lane == 0) mbar_arrive_expect_tx(full, n_box * box * D * 2);
             __syncwarp();
             if (mine) {
@@ -500,20 +506,33 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
    } else {
     // ============================================================ end of a bf16 item, or row parameters
     if constexpr (!Cfg::QUANT) {
-      // Rows of the last V tile past the piece's end become zeros (0 * NaN is NaN) before
-      // the MMAs see it.
-      uint32_t g = 0, phase = 0;
+      // V rows that some query row of the item does not see must not reach it as 0 * NaN.
+      // Those past the piece's end become zeros before the MMAs see them.  Of the others
+      // (the chunk's own tokens) what is not finite becomes zero, and the first such row
+      // is noted: query rows that see it end as NaN.
+      uint32_t g = 0, phase = 0, n_item = 0;
       each_item([&](const AttnItem& it, const Piece& pc, bool, int64_t) {
+        const int all_see = seen_by_all(it, pc);
+        int bad = INT_MAX;
+        int* noted = &bad_row[n_item++ & 3];     // no more than three items are in flight
         return each_stage(it, pc, [&](bool is_v, int j) {
           const int s = g++ % STAGES;
-          const int live = pc.end - (pc.r0 + j * BN);
-          if (!is_v || live >= BN) return true;
+          const int r = pc.r0 + j * BN, live = pc.end - r;
+          if (!is_v || r + BN <= all_see) return true;
           if (!wait_warp(&tail_full[s], (phase >> s) & 1, ctl)) return false;
           phase ^= 1u << s;
-          for (int i = lane; i < (BN - live) * (D / 8); i += 32)
-            *reinterpret_cast<uint4*>(smem + Cfg::OFF_KV + s * STAGE +
-                                      tile_off<BN>(live + i / (D / 8), i % (D / 8))) =
-                make_uint4(0, 0, 0, 0);
+          for (int i = max(0, all_see - r) * (D / 8) + lane; i < BN * (D / 8); i += 32) {
+            const int row = i / (D / 8);
+            uint4* at = reinterpret_cast<uint4*>(smem + Cfg::OFF_KV + s * STAGE +
+                                                 tile_off<BN>(row, i % (D / 8)));
+            if (row < live) {
+              if (bf16x8_finite(*at)) continue;
+              bad = min(bad, r + row);
+            }
+            *at = make_uint4(0, 0, 0, 0);
+          }
+          bad = __reduce_min_sync(0xffffffffu, bad);
+          if (lane == 0) *noted = bad;
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&kv_full[s]);
@@ -574,6 +593,9 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   reinterpret_cast<float*>(smem + Cfg::OFF_VSCALE)[2 * (v_tile % Cfg::V_RING) + h / 64] =
                       own_e ? INFINITY : static_cast<float>(hi);
               }
+              // a row of NaN: K's logits are; V's weights are (its e), for who sees it, and the
+              // row is zeros, as 0 * NaN would reach the others
+              const uint32_t not_a_row = is_v ? 0u : 0x7e007e00u;
               // K: one power of two for the 64 rows, the largest
               const int top_e = __reduce_max_sync(0xffffffffu, max(e[0], e[1]));
               const int ring = v_tile % Cfg::V_RING;
@@ -586,12 +608,12 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   const int x = is_v ? (zero[k] ? 0 : e[k] - ev[k]) : e[k] - top_e + 6;
                   const uint32_t f = x >= -14 ? static_cast<uint32_t>(x + 15) << 10
                                               : (x >= -24 ? 1u << (x + 24) : 0u);
-                  mul = nan[k] ? 0x7e007e00u : f | (f << 16);
+                  mul = nan[k] ? not_a_row : f | (f << 16);
                 } else {
                   // values below 2^(e + 1): to below 2^14 (K), below 2 (V)
                   const int x = is_v ? -ev[k] : 13 - top_e;
                   const float f = __uint_as_float(static_cast<uint32_t>(127 + x) << 23);
-                  mul = nan[k] ? 0x7e007e00u : pack_f16x2(bf16_lo(par[k]) * f, bf16_hi(par[k]) * f);
+                  mul = nan[k] ? not_a_row : pack_f16x2(bf16_lo(par[k]) * f, bf16_hi(par[k]) * f);
                 }
                 params[lane + 32 * k] = mul;
                 if (own_e) {
@@ -914,8 +936,9 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
 
       // ---- the item's result
       ok = ok && wait_warp(&o_full[t], n_item & 1, ctl);
-      ++n_item;
       tc_fence_after();
+      if (!Cfg::QUANT && pc.end > seen_by_all(it, pc) && bad_row[n_item & 3] < lim) l = NAN;
+      ++n_item;
       const float m2 = Cfg::QUANT || m == -INFINITY ? m : m * c;
       // Q's own block is no longer read; of rows that all groups share, block 1 never was
       float2* mls = reinterpret_cast<float2*>(smem + Cfg::OFF_ML +

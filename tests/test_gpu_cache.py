@@ -509,6 +509,28 @@ def test_non_finite_rows_reach_who_sees_them(kc, fmt, n_q):
     assert bool(torch.isfinite(out[1]).all())
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("G,n_q,bad", [(1, 3, 1), (4, 4, 3), (5, 33, 20), (2, 300, 0), (2, 300, 299), (4, 150, 77)])
+def test_non_finite_rows_of_later_tokens(kc, fmt, d, G, n_q, bad):
+    """A token whose own K and V rows are not finite: earlier tokens do not see them."""
+    lens = [n_q + 41, n_q]
+    c = filled(kc, fmt, lens, d, 32, seed=33)
+    k, v = rows_bf16(98, 2, 1, d), rows_bf16(99, 2, 1, d)
+    k[0, 0, 5] = float("nan")
+    v[0, 0, 3] = float("inf")
+    v[1, 0, d - 1] = float("nan")
+    at = torch.tensor([n - n_q + bad for n in lens], dtype=torch.int32, device="cuda")
+    c.write(k.cuda(), v.cuda(), starts=at)
+    c.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    q = rows_bf16(100, 2, G, n_q, d).cuda()
+    out = c.attend(q)
+    if bad:
+        check_attention(c, q[:, :, :bad], out[:, :, :bad], at.tolist(), [bad, bad])
+    assert not bool(torch.isfinite(out[0, :, bad:, 3]).any())
+    assert not bool(torch.isfinite(out[1, :, bad:, d - 1]).any())
+
+
 def test_captured_step_replays_with_growing_lengths(kc):
     """Append and attend in one CUDA graph: every replay adds a token."""
     for fmt in FMTS:
