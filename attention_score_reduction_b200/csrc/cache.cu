@@ -120,50 +120,65 @@ template <bool EXACT>
 __device__ __forceinline__ uint32_t int4_codes(const uint4& raw, const Int4Row& q) {
   constexpr float kRound = 12582912.f;
   constexpr uint32_t kRoundBits = 0x4b400000u;
-  float x[8];
-  unpack8(raw, x);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  const float2 lift = make_float2(q.lift, q.lift), zl = make_float2(q.zl, q.zl);
+  const float2 inv = make_float2(q.inv, q.inv), ns = make_float2(-q.s, -q.s);
   uint32_t word = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float d = fmaf(x[i], q.lift, q.zl);               // x - z
-    float t = d * q.inv;
-    t = fmaf(fmaf(-t, q.s, d), q.inv, t);
-    float u = t + kRound;
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+    const float2 d = ffma2(x, lift, zl);                    // x - z
+    float2 t = fmul2(d, inv);
+    t = ffma2(ffma2(t, ns, d), inv, t);
+    float2 u = fadd2(t, make_float2(kRound, kRound));
     if constexpr (EXACT) {
-      const float r = fmaf(kRound - u, q.s, d), half = 0.5f * q.s;
-      const bool odd = __float_as_uint(u) & 1u;
-      const float a = x[i] * q.lift, bb = d - a;
-      const float err = (a - (d - bb)) + (q.zl - bb);
-      if (r > half || (r == half && (err > 0.f || (err == 0.f && odd)))) u += 1.f;
-      if (r < -half || (r == -half && (err < 0.f || (err == 0.f && odd)))) u -= 1.f;
-      u = fminf(u, kRound + 15.f);
+      auto settle = [&](float xi, float di, float& ui) {
+        const float r = fmaf(kRound - ui, q.s, di), half = 0.5f * q.s;
+        const bool odd = __float_as_uint(ui) & 1u;
+        const float a = xi * q.lift, bb = di - a;
+        const float err = (a - (di - bb)) + (q.zl - bb);
+        if (r > half || (r == half && (err > 0.f || (err == 0.f && odd)))) ui += 1.f;
+        if (r < -half || (r == -half && (err < 0.f || (err == 0.f && odd)))) ui -= 1.f;
+        ui = fminf(ui, kRound + 15.f);
+      };
+      settle(x.x, d.x, u.x);
+      settle(x.y, d.y, u.y);
     }
-    word += (__float_as_uint(u) - kRoundBits) << (4 * i);
+    word += (__float_as_uint(u.x) - kRoundBits) << (8 * i);
+    word += (__float_as_uint(u.y) - kRoundBits) << (8 * i + 4);
   }
   return q.s > 0.f ? word : 0u;
 }
 
-// Stores N rows of which this lane has eight elements each; slot < 0: none.  Every step
+// Groups of eight elements that a lane has of a row, d / 8 / kGroups apart.  Quantised:
+// two, as half the shuffles and half the lanes that work out the row's scale.
+template <int FMT>
+constexpr int kGroups = FMT == kFmtBf16 ? 1 : 2;
+
+// Stores N rows of which this lane has C groups each; slot < 0: none.  Every step
 // goes over all rows before the next, so that their latencies overlap.
-template <int FMT, int D, int N>
+template <int FMT, int D, int N, int C>
 __device__ __forceinline__ void store_rows(uint8_t* pages, uint32_t* params, const int64_t (&slot)[N],
-                                           int lr, const uint4 (&raw)[N]) {
-  constexpr int LPR = D / 8;
+                                           int lr, const uint4 (&raw)[N][C]) {
+  constexpr int LPR = D / 8 / C;
   if constexpr (FMT == kFmtBf16) {
 #pragma unroll
     for (int n = 0; n < N; ++n)
       if (slot[n] >= 0)
-        *reinterpret_cast<uint4*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + lr * 16) = raw[n];
+        *reinterpret_cast<uint4*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + lr * 16) = raw[n][0];
   } else if constexpr (FMT == kFmtFp8) {
     // the largest magnitude by the order of the bits, where a NaN ranks above
     // infinity and so is seen
     uint32_t top[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
       uint32_t t = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) t = max(t, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+      for (int c = 0; c < C; ++c) {
+        const uint32_t w[4] = {raw[n][c].x, raw[n][c].y, raw[n][c].z, raw[n][c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = max(t, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+      }
       top[n] = t;
     }
 #pragma unroll
@@ -177,43 +192,63 @@ __device__ __forceinline__ void store_rows(uint8_t* pages, uint32_t* params, con
       e = top[n] == 0 ? 0 : max(e, -126);
       const bool bad = top[n] >= 0x7f800000u;
       const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);   // 2^-e
-      float x[8];
-      unpack8(raw[n], x);
-      uint32_t c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = pack_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-      if (slot[n] >= 0) {
+      for (int c = 0; c < C; ++c) {
+        float x[8];
+        unpack8(raw[n][c], x);
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = pack_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
         // a bad row's codes are zeros: NaN lives in parameters only, which the
         // attention applies after its mask
-        *reinterpret_cast<uint2*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + lr * 8) =
-            bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-        if (lr == 0)
-          params[slot[n]] = bad ? 0x7fc00000u : static_cast<uint32_t>(127 + e) << 23;
+        if (slot[n] >= 0)
+          *reinterpret_cast<uint2*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + (lr + c * LPR) * 8) =
+              bad ? make_uint2(0, 0) : make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
       }
+      if (slot[n] >= 0 && lr == 0)
+        params[slot[n]] = bad ? 0x7fc00000u : static_cast<uint32_t>(127 + e) << 23;
     }
   } else {
-    float lo[N], hi[N];
+    // (smallest, minus the largest) as two bf16, so that one exchange serves both
+    uint32_t ends[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      float x[8];
-      unpack8(raw[n], x);
-      lo[n] = fmin3_nan(fmin3_nan(x[0], x[1], x[2]), fmin3_nan(x[3], x[4], x[5]), fmin_nan(x[6], x[7]));
-      hi[n] = fmax3_nan(fmax3_nan(x[0], x[1], x[2]), fmax3_nan(x[3], x[4], x[5]), fmax_nan(x[6], x[7]));
+      uint32_t lo = raw[n][0].x, hi = raw[n][0].x;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const uint32_t w[4] = {raw[n][c].x, raw[n][c].y, raw[n][c].z, raw[n][c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lo = bf16x2_min_nan(lo, w[i]);
+          hi = bf16x2_max_nan(hi, w[i]);
+        }
+      }
+      hi ^= 0x80008000u;
+      ends[n] = bf16x2_min_nan(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
     }
 #pragma unroll
     for (int k = LPR / 2; k >= 1; k >>= 1)
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        lo[n] = fmin_nan(lo[n], __shfl_xor_sync(0xffffffffu, lo[n], k));
-        hi[n] = fmax_nan(hi[n], __shfl_xor_sync(0xffffffffu, hi[n], k));
-      }
+      for (int n = 0; n < N; ++n)
+        ends[n] = bf16x2_min_nan(ends[n], __shfl_xor_sync(0xffffffffu, ends[n], k));
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const Int4Row q = int4_row(lo[n], hi[n]);
-      uint32_t word = int4_codes<false>(raw[n], q);
-      if (q.exact) word = int4_codes<true>(raw[n], q);
+      const Int4Row q = int4_row(bf16_lo(ends[n]), -bf16_hi(ends[n]));
+      uint32_t word[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) word[c] = int4_codes<false>(raw[n][c], q);
+      if (q.exact) {
+#pragma unroll 1
+        for (int c = 0; c < C; ++c) {
+          const uint32_t exact = int4_codes<true>(c == 0 ? raw[n][0] : raw[n][C - 1], q);
+          if (c == 0) word[0] = exact; else word[C - 1] = exact;
+        }
+      }
       if (slot[n] >= 0) {
-        *reinterpret_cast<uint32_t*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + lr * 4) = word;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          *reinterpret_cast<uint32_t*>(pages + slot[n] * CacheRow<FMT, D>::BYTES + (lr + c * LPR) * 4) =
+              word[c];
         if (lr == 0) params[slot[n]] = q.par;
       }
     }
@@ -285,8 +320,9 @@ __device__ __forceinline__ uint4 row_values(const RowBits<FMT>& b) {
 template <int FMT, int D>
 __global__ void __launch_bounds__(kRowThreads, 4)
     cache_write_rows(const CacheWriteArgs a, int64_t total, int chunk, int mode) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, UNR = 2;
+  constexpr int C = kGroups<FMT>, LPR = D / 8 / C, RPW = 32 / LPR, UNR = FMT == kFmtFp8 ? 1 : 2;
   const int lane = threadIdx.x & 31;
+  cudaTriggerProgrammaticLaunchCompletion();   // the lengths' launch, if any, may begin; it waits
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   if (mode == 1) {
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
@@ -320,22 +356,28 @@ __global__ void __launch_bounds__(kRowThreads, 4)
   const uint16_t* vp = static_cast<const uint16_t*>(a.v) + lr * 8;
   for (int i0 = 0; i0 < chunk; i0 += UNR * RPW) {
     int64_t sl[UNR];
-    uint4 kr[UNR], vr[UNR];
+    uint4 kr[UNR][C], vr[UNR][C];
 #pragma unroll
     for (int j = 0; j < UNR; ++j) {
       const int i = i0 + j * RPW + sub;          // i >= chunk: its lane holds slot = -1, or i >= 32
       sl[j] = __shfl_sync(0xffffffffu, slot, i & 31);
-      kr[j] = ldg_stream16(kp + __shfl_sync(0xffffffffu, ksrc, i & 31));
-      vr[j] = ldg_stream16(vp + __shfl_sync(0xffffffffu, vsrc, i & 31));
+      const uint16_t* k1 = kp + __shfl_sync(0xffffffffu, ksrc, i & 31);
+      const uint16_t* v1 = vp + __shfl_sync(0xffffffffu, vsrc, i & 31);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        kr[j][c] = ldg_stream16(k1 + c * LPR * 8);
+        vr[j][c] = ldg_stream16(v1 + c * LPR * 8);
+      }
       if (i >= chunk) sl[j] = -1;
     }
-    store_rows<FMT, D, UNR>(static_cast<uint8_t*>(a.c.k_pages), a.c.k_params, sl, lr, kr);
-    store_rows<FMT, D, UNR>(static_cast<uint8_t*>(a.c.v_pages), a.c.v_params, sl, lr, vr);
+    store_rows<FMT, D, UNR, C>(static_cast<uint8_t*>(a.c.k_pages), a.c.k_params, sl, lr, kr);
+    store_rows<FMT, D, UNR, C>(static_cast<uint8_t*>(a.c.v_pages), a.c.v_params, sl, lr, vr);
   }
 }
 
 // Appends of many rows: lens moves on once every row has read the old one.
 __global__ void cache_advance(const CacheWriteArgs a) {
+  cudaGridDependencySynchronize();
   const int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (u < a.c.units) advance_len(a, u, held_to(a.c.lens[u], cache_cap(a.c), a.c.status));
 }
@@ -412,9 +454,17 @@ cudaError_t write_fd(const CacheWriteArgs& a, cudaStream_t s, int* launches) {
   *launches += 1;
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || mode != 0) return e;
-  cache_advance<<<static_cast<unsigned>((a.c.units + 127) / 128), 128, 0, s>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.c.units + 127) / 128));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // overlaps the launch latency
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
   *launches += 1;
-  return cudaGetLastError();
+  return cudaLaunchKernelEx(&cfg, cache_advance, a);
 }
 
 template <int FMT, int D>

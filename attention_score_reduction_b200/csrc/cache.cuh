@@ -47,6 +47,18 @@ __device__ __forceinline__ int64_t cache_slot(const CacheArgs& c, int64_t u, int
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// min and max of two bf16 each; NaN if one of them is
+__device__ __forceinline__ uint32_t bf16x2_min_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // none of eight bf16 is infinite or NaN
 __device__ __forceinline__ bool bf16x8_finite(const uint4& v) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
