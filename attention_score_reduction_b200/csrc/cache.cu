@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
     cache_write_rows(const CacheWriteArgs a, int64_t total, int chunk, int mode) {
   constexpr int C = kGroups<FMT>, LPR = D / 8 / C, RPW = 32 / LPR, UNR = FMT == kFmtFp8 ? 1 : 2;
   const int lane = threadIdx.x & 31;
-  cudaTriggerProgrammaticLaunchCompletion();   // the lengths' launch, if any, may begin; it waits
+  cudaTriggerProgrammaticLaunchCompletion();   // the next kernel may begin; it waits for this grid
+  cudaGridDependencySynchronize();
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   if (mode == 1) {
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
@@ -377,6 +378,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
 
 // Appends of many rows: lens moves on once every row has read the old one.
 __global__ void cache_advance(const CacheWriteArgs a) {
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int64_t u = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (u < a.c.units) advance_len(a, u, held_to(a.c.lens[u], cache_cap(a.c), a.c.status));
@@ -388,6 +390,8 @@ __global__ void __launch_bounds__(kRowThreads)
   // rows in flight: more where a row is few bytes
   constexpr int LPR = D / 8, RPW = 32 / LPR, UNR = FMT == kFmtInt4 ? 8 : 4;
   const int lane = threadIdx.x & 31;
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   const int64_t r0 = warp * chunk;
   int64_t slot = -1;
@@ -449,22 +453,12 @@ cudaError_t write_fd(const CacheWriteArgs& a, cudaStream_t s, int* launches) {
   int64_t blocks = (warps + per_block - 1) / per_block;
   if (blocks < 1) blocks = 1;     // no rows: lens may still change (starts given)
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  cache_write_rows<FMT, D><<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(a, total, chunk,
-                                                                                mode);
   *launches += 1;
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(cache_write_rows<FMT, D>, dim3(static_cast<unsigned>(blocks)),
+                                     kRowThreads, 0, s, a, total, chunk, mode);
   if (e != cudaSuccess || mode != 0) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.c.units + 127) / 128));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // overlaps the launch latency
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   *launches += 1;
-  return cudaLaunchKernelEx(&cfg, cache_advance, a);
+  return launch_after(cache_advance, dim3(static_cast<unsigned>((a.c.units + 127) / 128)), 128, 0, s, a);
 }
 
 template <int FMT, int D>
@@ -475,9 +469,9 @@ cudaError_t read_fd(const CacheReadArgs& a, cudaStream_t s, int* launches) {
   const int per_block = kRowThreads / 32;
   const int64_t blocks = (warps + per_block - 1) / per_block;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  cache_read_rows<FMT, D><<<static_cast<unsigned>(blocks), kRowThreads, 0, s>>>(a, total, chunk);
   *launches += 1;
-  return cudaGetLastError();
+  return launch_after(cache_read_rows<FMT, D>, dim3(static_cast<unsigned>(blocks)), kRowThreads, 0,
+                      s, a, total, chunk);
 }
 
 }  // namespace

@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
   const int64_t cta = blockIdx.x;
 
   cudaTriggerProgrammaticLaunchCompletion();   // the merge may be launched; it waits for this grid
+  cudaGridDependencySynchronize();
   Line<THREADS> line(a.c, shape, items, scratch, &spot_s);
   const int64_t all = line.all;
   const int64_t n_cta = line_ctas(all, gridDim.x);
@@ -692,9 +693,8 @@ cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st, int* launches) 
   cudaError_t e = cudaFuncSetAttribute(cache_attn_rows<FMT, D, NT>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::RING);
   if (e != cudaSuccess) return e;
-  cache_attn_rows<FMT, D, NT><<<ctas, Cfg::THREADS, Cfg::RING, st>>>(
-      a, shape, items, a.scale * 1.4426950408889634f, ml, o);
-  e = cudaGetLastError();
+  e = launch_after(cache_attn_rows<FMT, D, NT>, dim3(ctas), Cfg::THREADS, Cfg::RING, st, a, shape,
+                   items, a.scale * 1.4426950408889634f, ml, o);
   if (e != cudaSuccess) return e;
   *launches += 2;
   return launch_attn_merge(a, shape, items, ctas, false, ml, o, st);

@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   const Split sp = find_split(a, shape, items, ctas, by_item);
   const AttnItem& it = sp.it;
   cudaGridDependencySynchronize();       // the partial results are complete and visible
+  cudaTriggerProgrammaticLaunchCompletion();
 
   if (sp.parts > 0) {
     const int parts = sp.parts;
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   const Split sp = find_split(a, shape, items, ctas, by_item);
   const AttnItem& it = sp.it;
   cudaGridDependencySynchronize();       // the partial results are complete and visible
+  cudaTriggerProgrammaticLaunchCompletion();
 
   const int tasks = sp.parts > 0 ? ((it.rows + 31) / 32) * (D / 8) : 0;
   for (int task = blockIdx.y * kMergeWarps + warp; task < tasks; task += gridDim.y * kMergeWarps) {
@@ -303,26 +305,18 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
   int64_t y = cols ? (rows + 31) / 32 * (a.c.d / 8) / kMergeWarps
                    : (ctas > kWarpSplits * items ? rows : (rows + kMergeWarps - 1) / kMergeWarps);
   y = std::max<int64_t>(1, std::min<int64_t>(y, 148 * 8 / x));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // overlaps the launch latency
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
   if (cols) {
     const float4* o4 = reinterpret_cast<const float4*>(o);
-    return a.c.d == 128 ? cudaLaunchKernelEx(&cfg, cache_attn_merge_cols<128>, a, shape, items, ctas,
-                                             by_item, ml, o4)
-                        : cudaLaunchKernelEx(&cfg, cache_attn_merge_cols<256>, a, shape, items, ctas,
-                                             by_item, ml, o4);
+    return a.c.d == 128 ? launch_after(cache_attn_merge_cols<128>, grid, kMergeThreads, 0, st, a, shape, items, ctas,
+                                       by_item, ml, o4)
+                        : launch_after(cache_attn_merge_cols<256>, grid, kMergeThreads, 0, st, a, shape, items, ctas,
+                                       by_item, ml, o4);
   }
-  return a.c.d == 128 ? cudaLaunchKernelEx(&cfg, cache_attn_merge<128>, a, shape, items, ctas,
-                                           by_item, ml, o)
-                      : cudaLaunchKernelEx(&cfg, cache_attn_merge<256>, a, shape, items, ctas,
-                                           by_item, ml, o);
+  return a.c.d == 128 ? launch_after(cache_attn_merge<128>, grid, kMergeThreads, 0, st, a, shape, items, ctas,
+                                       by_item, ml, o)
+                      : launch_after(cache_attn_merge<256>, grid, kMergeThreads, 0, st, a, shape, items, ctas,
+                                       by_item, ml, o);
 }
 
 // Up to 16 query rows a unit go to the mma.sync kernel, which reads the cache once

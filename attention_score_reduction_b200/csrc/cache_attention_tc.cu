@@ -116,7 +116,7 @@ struct TcaCfg {
   // raw_empty[RAW_SLOTS]
   static constexpr int N_BARS = 3 * STAGES + 13 + 3 * RAW_SLOTS;
   static constexpr int OFF_MISC = OFF_BAR + 8 * N_BARS;
-  static constexpr int BYTES = OFF_MISC + 32;          // TMEM address, abort flag, bad rows of four items
+  static constexpr int BYTES = OFF_MISC + 48;          // TMEM address, abort flag, bad rows of four items
   static constexpr int SMEM = BYTES + 1024;
   static_assert(SMEM <= 232448 - 256, "exceeds 227 KB of shared memory with the static part");
   // registers a thread of each warpgroup after the split (0: no split); the sums
@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
   const int64_t cta = blockIdx.x;
 
   cudaTriggerProgrammaticLaunchCompletion();   // the merge may be launched; it waits for this grid
+  cudaGridDependencySynchronize();
   Line<THREADS> line(a.c, shape, items, scratch, &spot_s);
   const int64_t all = line.all;
   const int64_t n_cta = line_ctas(all, gridDim.x);
@@ -509,12 +510,12 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
       // V rows that some query row of the item does not see must not reach it as 0 * NaN.
       // Those past the piece's end become zeros before the MMAs see them.  Of the others
       // (the chunk's own tokens) what is not finite becomes zero, and the first such row
-      // is noted: query rows that see it end as NaN.
+      // is noted, by the parity of its tile: query rows that see it end as NaN.
       uint32_t g = 0, phase = 0, n_item = 0;
       each_item([&](const AttnItem& it, const Piece& pc, bool, int64_t) {
         const int all_see = seen_by_all(it, pc);
         int bad = INT_MAX;
-        int* noted = &bad_row[n_item++ & 3];     // no more than three items are in flight
+        int* noted = &bad_row[2 * (n_item++ & 3)];     // no more than three items are in flight
         return each_stage(it, pc, [&](bool is_v, int j) {
           const int s = g++ % STAGES;
           const int r = pc.r0 + j * BN, live = pc.end - r;
@@ -532,7 +533,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
             *at = make_uint4(0, 0, 0, 0);
           }
           bad = __reduce_min_sync(0xffffffffu, bad);
-          if (lane == 0) *noted = bad;
+          if (lane == 0) noted[j & 1] = bad;
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&kv_full[s]);
@@ -937,7 +938,15 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
       // ---- the item's result
       ok = ok && wait_warp(&o_full[t], n_item & 1, ctl);
       tc_fence_after();
-      if (!Cfg::QUANT && pc.end > seen_by_all(it, pc) && bad_row[n_item & 3] < lim) l = NAN;
+      if constexpr (!Cfg::QUANT) {
+        // notes of tiles whose output this group has waited for: all, or of one parity
+        const int first = max(seen_by_all(it, pc) - pc.r0, 0) / BN;       // ragged tile
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          if ((!join || p == t) && first + ((first ^ p) & 1) < pc.n &&
+              bad_row[2 * (n_item & 3) + p] < lim)
+            l = NAN;
+      }
       ++n_item;
       const float m2 = Cfg::QUANT || m == -INFINITY ? m : m * c;
       // Q's own block is no longer read; of rows that all groups share, block 1 never was
@@ -1132,9 +1141,8 @@ cudaError_t launch_tc_fd(const CacheAttnArgs& a, cudaStream_t st, int* launches)
     }();
     if (regs < Cfg::R_LAUNCH) return cudaErrorLaunchOutOfResources;
   }
-  cache_attn_tc<FMT, D><<<kTcCtas, Cfg::THREADS, Cfg::SMEM, st>>>(
-      kmap, vmap, a, shape, items, a.scale * 1.4426950408889634f, ml, o);
-  e = cudaGetLastError();
+  e = launch_after(cache_attn_tc<FMT, D>, dim3(kTcCtas), Cfg::THREADS, Cfg::SMEM, st, kmap, vmap, a,
+                   shape, items, a.scale * 1.4426950408889634f, ml, o);
   if (e != cudaSuccess) return e;
   *launches += 2;
   return launch_attn_merge(a, shape, items, kTcCtas, true, ml, o, st);

@@ -562,6 +562,78 @@ def test_captured_step_replays_with_growing_lengths(kc):
                 check_stored(c, "k", u, lens[u] - 1, k[u])
 
 
+def test_captured_behind_a_fork(kc):
+    """Calls captured where two streams have joined: a launch has two predecessors."""
+    for fmt in FMTS:
+        c = filled(kc, fmt, [70, 9], 128, 16, seed=15, capacity=90)
+        k, v = rows_bf16(140, 2, 1, 128).cuda(), rows_bf16(141, 2, 1, 128).cuda()
+        q = rows_bf16(142, 2, 4, 1, 128).cuda()
+        kk, vv, out = torch.empty_like(k), torch.empty_like(v), torch.empty_like(q)
+        back = torch.zeros(2, 80, 128, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(g):
+            main = torch.cuda.current_stream()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                kk.copy_(k)
+            vv.copy_(v)
+            main.wait_stream(side)
+            c.write(kk, vv)
+            side.wait_stream(main)
+            c.attend(q, out=out)
+            c.read(n_rows=80, k_out=back, v_out=torch.empty_like(back), stream=side)
+            main.wait_stream(side)
+        g.replay()
+        g.replay()
+        lens = [72, 11]
+        assert c.lens.tolist() == lens
+        check_attention(c, q, out, lens, [1, 1])
+        assert np.array_equal(f64(back[0, :72]), held_values(c, "k", 0, 72)) or fmt == "int4"
+        del g
+
+
+@pytest.mark.parametrize("n_q", [1, 20])
+@pytest.mark.parametrize("fmt", ["bf16", "int4"])
+def test_more_units_than_threads(kc, fmt, n_q):
+    """A block finds its place among more items than it has threads."""
+    g = torch.Generator().manual_seed(16)
+    lens = torch.randint(0, 50, (700,), generator=g).tolist()
+    lens[3], lens[650], lens[699] = 2500, 1300, 700
+    c = filled(kc, fmt, lens, 128, 32, seed=16)
+    q = rows_bf16(143, len(lens), 2, n_q, 128).cuda()
+    q_lens = [min(n_q, n) for n in lens]
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    c.attend(q, q_lens=torch.tensor(q_lens, dtype=torch.int32, device="cuda"), out=out)
+    c.check_status()
+    some = [0, 1, 2, 3, 4, 255, 256, 257, 300, 639, 640, 649, 650, 651, 698, 699]
+    for u in some:
+        one = kc.PagedCache(c.fmt, c.k_pages, c.v_pages, c.k_params, c.v_params,
+                            c.page_table[u:u + 1], c.lens[u:u + 1])
+        check_attention(one, q[u:u + 1], out[u:u + 1], [lens[u]], [q_lens[u]], untouched=7.0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [128, 256])
+def test_stalled_waits_end_and_are_recorded(kc, kz, fmt, d):
+    """With the loads left out every wait runs out (10 ms here); the next call is right."""
+    c = filled(kc, fmt, [900, 300], d, 32, seed=17)
+    q = rows_bf16(144, 2, 4, 40, d).cuda()
+    want = c.attend(q)
+    c.check_status()
+    kz.set_wait_timeout_ns(10_000_000)
+    kz.set_test_stall(True)
+    try:
+        c.attend(q)
+        status = kz.workspace_status(c.status)
+    finally:
+        kz.set_test_stall(False)
+        kz.set_wait_timeout_ns(0)
+    assert status == kz.ERR_TIMEOUT
+    assert torch.equal(c.attend(q), want)
+    c.check_status()
+
+
 def test_two_captured_graphs_at_once(kc):
     """Two graphs of calls on the same cache, replayed on two streams together."""
     c = filled(kc, "fp8", [3000, 100], 128, 64, seed=12)
