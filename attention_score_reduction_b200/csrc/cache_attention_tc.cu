@@ -132,9 +132,9 @@ struct TcaCfg {
   // quantised: one power of two for 64 rows of V where it will do, instead of one a row.
   // d = 128: a seventh faster; d = 256: as fast with either, the plainer one
   static constexpr bool ONE_E = QUANT && D == 128;
-  // of 8 pairs of exponentials, those on the FMA pipe (beside the unpacking at d = 128,
-  // issue slots are scarcer)
-  static constexpr int POLY = ONE_E ? 0 : 2;
+  // of 8 pairs of exponentials, those on the FMA pipe (beside the unpacking, issue slots
+  // are scarcer: none there is up to a tenth faster than two)
+  static constexpr int POLY = QUANT ? 0 : 2;
 };
 
 // Shared-memory matrix descriptors under the 128-byte swizzle, low words (the high
