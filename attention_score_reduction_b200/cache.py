@@ -23,6 +23,11 @@ import torch
 from . import kvzip as kz
 
 
+# the current stream's handle without the Stream object around it (1.2 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class PagedCache:
     """Pools, page table and lengths of one layer's cache, on one GPU.
 
@@ -120,7 +125,7 @@ class PagedCache:
         usual case, both current already, costs no context switches: a decoding
         step's calls are short enough for the host's time to show."""
         if stream is None and torch.cuda.current_device() == self._index:
-            return call(*args, torch.cuda.current_stream(self._index).cuda_stream)
+            return call(*args, _raw_stream(self._index))
         with self._on(stream) as st:
             return call(*args, st)
 
