@@ -36,7 +36,7 @@ __device__ __forceinline__ int held_to(int64_t n, int hi, uint32_t* status) {
 // Pool row of position pos of unit u (0 <= pos < max_pages * page_rows), or -1
 // (and the status bit) where the page table names no page of the pool.
 __device__ __forceinline__ int64_t cache_slot(const CacheArgs& c, int64_t u, int pos) {
-  const int page = c.page_table[u * c.max_pages + (pos >> c.page_shift)];
+  const int page = __ldcg(c.page_table + u * c.max_pages + (pos >> c.page_shift));
   if (page < 0 || page >= c.n_pages) {
     atomicOr(c.status, kStatusBadCache);
     return -1;
@@ -47,7 +47,18 @@ __device__ __forceinline__ int64_t cache_slot(const CacheArgs& c, int64_t u, int
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Launch of a kernel that begins with cudaGridDependencySynchronize(): its start overlaps
+// First thing in a kernel launched by launch_after: waits for the kernel before it, then
+// lets the next one be launched.  Not the other way round: three kernels of a stream would
+// be on an SM together, and the third could find lines in L1 that the first had loaded and
+// the second has since written.  For the same reason what an earlier kernel of the stream
+// may have written is read through L2 (ld_l2_*, __ldcg, asynchronous copies), never by
+// read-only loads.
+__device__ __forceinline__ void begin_after_previous() {
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+}
+
+// Launch of a kernel that begins with begin_after_previous(): its start overlaps
 // the end of the kernel before it on the stream.
 template <typename... Params, typename... Args>
 inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int block, size_t smem,
@@ -155,19 +166,18 @@ __device__ __forceinline__ uint32_t nib_f16x2(uint32_t w) {
     return hfma2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd400d400u);   // / 16 - 64
 }
 
-// 16-byte read-only load that is not kept in L1 (each cache byte is used once per CTA)
-__device__ __forceinline__ uint4 ldg_stream16(const void* p) {
+// loads through L2 (each cache byte is used once per CTA)
+__device__ __forceinline__ uint4 ld_l2_16(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
+__device__ __forceinline__ uint2 ld_l2_8(const void* p) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
+  asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
   return v;
 }
 

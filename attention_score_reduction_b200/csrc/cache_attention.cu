@@ -16,7 +16,15 @@
 // interleaved with byte permutes.  The accumulator fragment of S is the B
 // fragment of P^T as it stands.  Each warp keeps a ring of two or three batches in
 // shared memory that asynchronous copies fill, so that over 100 KB per SM are in
-// flight; batches held in registers (one ahead) reached half of that.
+// flight; batches held in registers (one ahead) reached half of that.  Two or three
+// CTAs an SM: more start and end more items' parts, fewer leave issue slots idle
+// (16 sequences, 4-bit, 2 / 3 / 4 CTAs an SM: 64 / 58 / 60 us; bf16, 2 with three
+// batches 39 us, 3 with two 41 us).
+//
+// Measured, a call in a stream: one token over a bf16 layer of 62K rows a head at most
+// (145 MB) 34 us, of which 27 go to the loads (5.4 TB/s; CTAs end between 23 and 31 us,
+// as some SMs get more of HBM than others) and the rest to start, join and merge; one
+// token for each of 16 sequences over 4-bit pages (149 MB) 47 us, bound by issue slots.
 //
 // Quantised formats multiply the codes themselves, as fp16, and fold the rows'
 // parameters into logits and weights:
@@ -160,8 +168,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
   const int quad = lane >> 2, qp = lane & 3;
   const int64_t cta = blockIdx.x;
 
-  cudaTriggerProgrammaticLaunchCompletion();   // the merge may be launched; it waits for this grid
-  cudaGridDependencySynchronize();
+  begin_after_previous();
   Line<THREADS> line(a.c, shape, items, scratch, &spot_s);
   const int64_t all = line.all;
   const int64_t n_cta = line_ctas(all, gridDim.x);
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
         const int el = FMT == kFmtInt4 ? 128 * (ks / 8) + 32 * qp + 4 * (ks % 8)
                        : FMT == kFmtBf16 ? 32 * (ks / 2) + 8 * qp
                                          : 64 * (ks / 4) + 16 * qp + 4 * (ks & 3);
-        if (live) v = *reinterpret_cast<const uint4*>(qr + el);
+        if (live) v = __ldcg(reinterpret_cast<const uint4*>(qr + el));
         qa[ks][2 * t] = v.x;
         qa[ks][2 * t + 1] = v.y;
         qa[ks + 1][2 * t] = v.z;

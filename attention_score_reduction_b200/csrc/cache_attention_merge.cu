@@ -28,7 +28,7 @@ __device__ __forceinline__ void add_part(RowPart<D>& acc, const float* o, float 
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < D / 128; ++i) {
-    const float4 x = reinterpret_cast<const float4*>(o)[lane + 32 * i];
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(o) + lane + 32 * i);
     acc.v[i].x = fmaf(x.x, f, acc.v[i].x);
     acc.v[i].y = fmaf(x.y, f, acc.v[i].y);
     acc.v[i].z = fmaf(x.z, f, acc.v[i].z);
@@ -122,21 +122,20 @@ __device__ __forceinline__ void put_zeros(const CacheAttnArgs& a, const AttnShap
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     cache_attn_merge(const CacheAttnArgs a, const AttnShape shape, int64_t items, int ctas,
-                     int by_item, const float2* __restrict__ ml, const float* __restrict__ o) {
+                     int by_item, const float2* ml, const float* o) {
   __shared__ RowPart<D> acc_s[kMergeWarps][32];
   __shared__ float l_s[kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Split sp = find_split(a, shape, items, ctas, by_item);
   const AttnItem& it = sp.it;
-  cudaGridDependencySynchronize();       // the partial results are complete and visible
-  cudaTriggerProgrammaticLaunchCompletion();
+  begin_after_previous();                // the partial results are complete and visible
 
   if (sp.parts > 0) {
     const int parts = sp.parts;
     auto part = [&](int i) { return sp.slot(i) * shape.block; };
     if (parts <= kWarpSplits) {
       for (int row = blockIdx.y * kMergeWarps + warp; row < it.rows; row += gridDim.y * kMergeWarps) {
-        const float2 x = lane < parts ? ml[part(lane) + row] : make_float2(-INFINITY, 0.f);
+        const float2 x = lane < parts ? __ldcg(ml + part(lane) + row) : make_float2(-INFINITY, 0.f);
         float M = x.x;
 #pragma unroll
         for (int k = 16; k >= 1; k >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, k));
@@ -161,17 +160,17 @@ __global__ void __launch_bounds__(kMergeThreads)
           const int i = warp + k * kMergeWarps;
           if (i < parts) {
             const int64_t slot = part(i) + row;
-            xl[k] = ml[slot];
+            xl[k] = __ldcg(ml + slot);
 #pragma unroll
             for (int e = 0; e < D / 128; ++e)
-              x[k].v[e] = reinterpret_cast<const float4*>(o + slot * D)[lane + 32 * e];
+              x[k].v[e] = __ldcg(reinterpret_cast<const float4*>(o + slot * D) + lane + 32 * e);
           } else {
             xl[k] = make_float2(-INFINITY, 0.f);
             x[k] = {};
           }
         }
         float M = -INFINITY;
-        for (int i = lane; i < parts; i += 32) M = fmax_nan(M, ml[part(i) + row].x);
+        for (int i = lane; i < parts; i += 32) M = fmax_nan(M, __ldcg(ml + part(i) + row).x);
 #pragma unroll
         for (int k = 16; k >= 1; k >>= 1) M = fmax_nan(M, __shfl_xor_sync(0xffffffffu, M, k));
         const float sub = M == -INFINITY ? 0.f : M;
@@ -195,8 +194,8 @@ __global__ void __launch_bounds__(kMergeThreads)
           RowPart<D> y;
 #pragma unroll
           for (int e = 0; e < D / 128; ++e)
-            y.v[e] = reinterpret_cast<const float4*>(o + slot * D)[lane + 32 * e];
-          add(y, ml[slot]);
+            y.v[e] = __ldcg(reinterpret_cast<const float4*>(o + slot * D) + lane + 32 * e);
+          add(y, __ldcg(ml + slot));
         }
         acc_s[warp][lane] = acc;
         if (lane == 0) l_s[warp] = L;
@@ -230,14 +229,13 @@ __global__ void __launch_bounds__(kMergeThreads)
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     cache_attn_merge_cols(const CacheAttnArgs a, const AttnShape shape, int64_t items, int ctas,
-                          int by_item, const float2* __restrict__ ml,
-                          const float4* __restrict__ o) {
+                          int by_item, const float2* ml,
+                          const float4* o) {
   constexpr int AHEAD = 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Split sp = find_split(a, shape, items, ctas, by_item);
   const AttnItem& it = sp.it;
-  cudaGridDependencySynchronize();       // the partial results are complete and visible
-  cudaTriggerProgrammaticLaunchCompletion();
+  begin_after_previous();                // the partial results are complete and visible
 
   const int tasks = sp.parts > 0 ? ((it.rows + 31) / 32) * (D / 8) : 0;
   for (int task = blockIdx.y * kMergeWarps + warp; task < tasks; task += gridDim.y * kMergeWarps) {
@@ -255,10 +253,10 @@ __global__ void __launch_bounds__(kMergeThreads)
         p[k] = q[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i0 + k < sp.parts) {
           const int64_t s = sp.slot(i0 + k);
-          x[k] = ml[s * shape.block + row];
+          x[k] = __ldcg(ml + s * shape.block + row);
           const float4* part = o + (s * (D / 4) + 2 * chunk) * shape.block + row;
-          p[k] = part[0];
-          q[k] = part[shape.block];
+          p[k] = __ldcg(part);
+          q[k] = __ldcg(part + shape.block);
         }
       }
 #pragma unroll

@@ -45,8 +45,8 @@ __device__ __forceinline__ AttnItem attn_item(const CacheArgs& c, const AttnShap
   AttnItem it;
   it.u = static_cast<uint32_t>(w) / static_cast<uint32_t>(s.blocks);   // w < 2^31
   const int b = static_cast<int>(w - it.u * s.blocks);
-  it.len = held_to(c.lens[it.u], cache_cap(c), c.status);
-  it.m = s.q_lens ? held_to(s.q_lens[it.u], s.n_q, c.status) : s.n_q;
+  it.len = held_to(__ldcg(c.lens + it.u), cache_cap(c), c.status);
+  it.m = s.q_lens ? held_to(__ldcg(s.q_lens + it.u), s.n_q, c.status) : s.n_q;
   it.row0 = b * s.block;
   it.rows = min(s.block, it.m * s.G - it.row0);
   it.vis = 0;

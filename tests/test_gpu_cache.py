@@ -634,6 +634,56 @@ def test_stalled_waits_end_and_are_recorded(kc, kz, fmt, d):
     c.check_status()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [128, 256])
+def test_same_bits_where_blocks_cross_items(kc, fmt, d):
+    """Many long items, several to a block: pages, tiles and parameters of one item come
+    while the one before is still worked on."""
+    g = torch.Generator().manual_seed(19)
+    lens = torch.randint(310, 5000, (32,), generator=g).tolist()
+    c = filled(kc, fmt, lens, d, 128, seed=19)
+    q = rows_bf16(170, 32, 4, 301, d).cuda()
+    ql = torch.tensor([301 - 7 * (u // 8) for u in range(32)], dtype=torch.int32, device="cuda")
+    outs = [torch.zeros_like(q) for _ in range(30)]
+    for o in outs:
+        c.attend(q, q_lens=ql, out=o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    for u in (0, 17, 31):
+        one = kc.PagedCache(c.fmt, c.k_pages, c.v_pages, c.k_params, c.v_params,
+                            c.page_table[u:u + 1], c.lens[u:u + 1])
+        check_attention(one, q[u:u + 1], outs[0][u:u + 1], [lens[u]], [int(ql[u])], untouched=0.0)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,n_q", [(128, 1), (128, 150), (256, 1), (256, 90)])
+def test_calls_back_to_back(kc, fmt, d, n_q):
+    """Calls that follow one another without a pause, through the same scratch memory:
+    each gives the bits that it gives alone."""
+    lens = [5000, 1200, 3333, 40]
+    c = filled(kc, fmt, lens, d, 32, seed=18)
+    qs = [rows_bf16(150 + i, 4, 4, n_q, d).cuda() for i in range(3)]
+    k, v = (rows_bf16(160 + i, 4, 3, d).cuda() for i in range(2))
+    start = torch.tensor([n - 3 for n in lens], dtype=torch.int32).cuda()
+    want = []
+    for i, q in enumerate(qs):
+        c.write(k * (i + 1), v * (i + 1), starts=start)
+        torch.cuda.synchronize()
+        want.append(c.attend(q))
+        torch.cuda.synchronize()
+    news = [(k * (i + 1), v * (i + 1)) for i in range(3)]
+    outs = [[torch.empty_like(q) for q in qs] for _ in range(40)]
+    torch.cuda.synchronize()
+    for step in outs:
+        for q, o, (kn, vn) in zip(qs, step, news):
+            c.write(kn, vn, starts=start)
+            c.attend(q, out=o)
+    torch.cuda.synchronize()
+    for step in outs:
+        for o, w in zip(step, want):
+            assert torch.equal(o, w)
+
+
 def test_two_captured_graphs_at_once(kc):
     """Two graphs of calls on the same cache, replayed on two streams together."""
     c = filled(kc, "fp8", [3000, 100], 128, 64, seed=12)
