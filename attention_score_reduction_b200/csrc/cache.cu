@@ -50,23 +50,23 @@ __device__ __forceinline__ bool row_owner(const int64_t* offsets, int64_t units,
   int64_t lo = 0, hi = units;            // offsets[lo] <= r (or lo = 0), r < offsets[hi] (or hi = units)
   while (hi - lo > 1) {
     const int64_t mid = (lo + hi) >> 1;
-    if (__ldcg(offsets + mid) <= r) lo = mid; else hi = mid;
+    if (offsets[mid] <= r) lo = mid; else hi = mid;
   }
   *u = lo;
-  *t = r - __ldcg(offsets + lo);
-  return *t >= 0 && r < __ldcg(offsets + lo + 1);
+  *t = r - offsets[lo];
+  return *t >= 0 && r < offsets[lo + 1];
 }
 
 // Rows the call brings for unit u.
 __device__ __forceinline__ int64_t rows_of(const CacheWriteArgs& a, int64_t u) {
   if (a.offsets != nullptr) {
-    const int64_t lo = __ldcg(a.offsets + u), hi = __ldcg(a.offsets + u + 1);
+    const int64_t lo = a.offsets[u], hi = a.offsets[u + 1];
     if (lo < 0 || hi < lo || hi > a.n_rows) atomicOr(a.c.status, kStatusBadCache);
     const int64_t n = (hi > a.n_rows ? a.n_rows : hi) - (lo < 0 ? 0 : lo);
     return n < 0 ? 0 : n;
   }
   return a.counts == nullptr ? a.n_rows
-                             : held_to(__ldcg(a.counts + u), static_cast<int>(a.n_rows), a.c.status);
+                             : held_to(a.counts[u], static_cast<int>(a.n_rows), a.c.status);
 }
 
 __device__ __forceinline__ void advance_len(const CacheWriteArgs& a, int64_t u, int first) {
@@ -267,16 +267,16 @@ __device__ __forceinline__ RowBits<FMT> load_row(const uint8_t* pages, const uin
   RowBits<FMT> b{};
   const uint8_t* p = pages + slot * CacheRow<FMT, D>::BYTES;
   if constexpr (FMT == kFmtBf16) {
-    b.c = ld_l2_16(p + lr * 16);
+    b.c = ld_stream16(p + lr * 16);
   } else {
     if constexpr (FMT == kFmtFp8) {
-      const uint2 v = ld_l2_8(p + lr * 8);
+      const uint2 v = ld_stream8(p + lr * 8);
       b.c.x = v.x;
       b.c.y = v.y;
     } else {
-      b.c.x = __ldcg(reinterpret_cast<const uint32_t*>(p + lr * 4));
+      b.c.x = ld_stream4(p + lr * 4);
     }
-    b.par = __ldcg(params + slot);
+    b.par = ld_stream4(params + slot);
   }
   return b;
 }
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
     const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; u < a.c.units;
          u += step)
-      advance_len(a, u, held_to(__ldcg(a.starts + u), cache_cap(a.c), a.c.status));
+      advance_len(a, u, held_to(a.starts[u], cache_cap(a.c), a.c.status));
   }
   const int64_t r0 = warp * chunk;
   // lane i: where row r0 + i comes from and goes to
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
     if (row_owner(a.offsets, a.c.units, a.n_rows, r0 + lane, &u, &t) && t < rows_of(a, u)) {
       const int cap = cache_cap(a.c);
       const int64_t pos =
-          held_to(__ldcg(a.starts ? a.starts + u : a.c.lens + u), cap, a.c.status) + t;
+          held_to(a.starts ? a.starts[u] : __ldcg(a.c.lens + u), cap, a.c.status) + t;
       if (pos < cap)
         slot = cache_slot(a.c, u, static_cast<int>(pos));
       else
@@ -366,8 +366,8 @@ __global__ void __launch_bounds__(kRowThreads, 4)
       const uint16_t* v1 = vp + __shfl_sync(0xffffffffu, vsrc, i & 31);
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        kr[j][c] = ld_l2_16(k1 + c * LPR * 8);
-        vr[j][c] = ld_l2_16(v1 + c * LPR * 8);
+        kr[j][c] = ld_stream16(k1 + c * LPR * 8);
+        vr[j][c] = ld_stream16(v1 + c * LPR * 8);
       }
       if (i >= chunk) sl[j] = -1;
     }
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kRowThreads)
     int64_t u, t;
     if (row_owner(a.offsets, a.c.units, a.n_rows, r0 + lane, &u, &t)) {
       const int cap = cache_cap(a.c);
-      const int64_t pos = (a.starts ? held_to(__ldcg(a.starts + u), cap, a.c.status) : 0) + t;
+      const int64_t pos = (a.starts ? held_to(a.starts[u], cap, a.c.status) : 0) + t;
       if (pos < held_to(__ldcg(a.c.lens + u), cap, a.c.status))
         slot = cache_slot(a.c, u, static_cast<int>(pos));
     }

@@ -36,7 +36,7 @@ __device__ __forceinline__ int held_to(int64_t n, int hi, uint32_t* status) {
 // Pool row of position pos of unit u (0 <= pos < max_pages * page_rows), or -1
 // (and the status bit) where the page table names no page of the pool.
 __device__ __forceinline__ int64_t cache_slot(const CacheArgs& c, int64_t u, int pos) {
-  const int page = __ldcg(c.page_table + u * c.max_pages + (pos >> c.page_shift));
+  const int page = c.page_table[u * c.max_pages + (pos >> c.page_shift)];
   if (page < 0 || page >= c.n_pages) {
     atomicOr(c.status, kStatusBadCache);
     return -1;
@@ -50,9 +50,9 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // First thing in a kernel launched by launch_after: waits for the kernel before it, then
 // lets the next one be launched.  Not the other way round: three kernels of a stream would
 // be on an SM together, and the third could find lines in L1 that the first had loaded and
-// the second has since written.  For the same reason what an earlier kernel of the stream
-// may have written is read through L2 (ld_l2_*, __ldcg, asynchronous copies), never by
-// read-only loads.
+// the second has since written.  For the same reason what this file's kernels write (pages,
+// parameters, lengths, partial results, outputs) is read by loads that leave nothing in L1
+// (ld_stream*, __ldcg, asynchronous copies), never by read-only ones.
 __device__ __forceinline__ void begin_after_previous() {
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();
@@ -166,18 +166,22 @@ __device__ __forceinline__ uint32_t nib_f16x2(uint32_t w) {
     return hfma2(and_or(w, 0x00f000f0u, 0x64006400u), 0x2c002c00u, 0xd400d400u);   // / 16 - 64
 }
 
-// loads through L2 (each cache byte is used once per CTA)
-__device__ __forceinline__ uint4 ld_l2_16(const void* p) {
+// loads that are not kept in L1 (each byte is used once)
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
   uint4 v;
-  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
+               : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint2 ld_l2_8(const void* p) {
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
   uint2 v;
-  asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_stream4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 
