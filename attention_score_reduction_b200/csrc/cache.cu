@@ -316,8 +316,8 @@ __device__ __forceinline__ uint4 row_values(const RowBits<FMT>& b) {
 // any thread may write lens; 2: append, a warp's chunk is one whole unit.
 // Rows that are not there load from the first row instead (no branch between loads).
 // Two rows of K and of V per step (fp8: one): at four the 4-bit kernel spills or loses
-// half of its warps.  62000 rows a head of 8, packed, to 4-bit pages and back as bf16 (two
-// launches, 296 MB): 71 us, 4.2 TB/s; one row a step 77, one group a lane 87.
+// half of its warps.  255K packed rows to 4-bit pages and back as bf16 (two launches,
+// 296 MB): 71 us, 4.2 TB/s; one row a step 77, one group a lane 87.
 template <int FMT, int D>
 __global__ void __launch_bounds__(kRowThreads, 4)
     cache_write_rows(const CacheWriteArgs a, int64_t total, int chunk, int mode) {

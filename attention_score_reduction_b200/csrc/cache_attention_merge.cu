@@ -36,25 +36,25 @@ __device__ __forceinline__ void add_part(RowPart<D>& acc, const float* o, float 
   }
 }
 
-// out row = acc / L (0 where L is 0), four elements a lane.
+// Elements e .. e + 3 of an output row: x / L (0 where L is 0).
+__device__ __forceinline__ void put4(const CacheAttnArgs& a, const AttnShape& s, const AttnItem& it,
+                                     int row, int e, float4 x, float L) {
+  const int r = it.row0 + row, tok = r / s.G, g = r - tok * s.G;
+  const int64_t at = it.u * a.o_unit + g * a.o_head + tok * a.o_row + e;
+  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+  x = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+               : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  if (a.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = x;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+}
 template <int D>
 __device__ __forceinline__ void put_row(const CacheAttnArgs& a, const AttnShape& s,
                                         const AttnItem& it, int row, const RowPart<D>& acc, float L) {
-  const int lane = threadIdx.x & 31;
-  const int r = it.row0 + row, tok = r / s.G, g = r - tok * s.G;
-  const int64_t at = it.u * a.o_unit + g * a.o_head + tok * a.o_row + 4 * lane;
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
 #pragma unroll
-  for (int i = 0; i < D / 128; ++i) {
-    float4 x = acc.v[i];
-    x = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                 : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    if (a.out_f32)
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + 128 * i) = x;
-    else
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + 128 * i) =
-          make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-  }
+  for (int i = 0; i < D / 128; ++i) put4(a, s, it, row, 4 * (threadIdx.x & 31) + 128 * i, acc.v[i], L);
 }
 
 // Which item a block joins does not depend on the results, so it is found before
@@ -223,40 +223,39 @@ __global__ void __launch_bounds__(kMergeThreads)
 }
 
 // Parts of the tensor-memory kernel: a slot's o is [D / 4][block] of four elements, as its
-// threads (a query row each) can store it with whole lines; a warp joins 32 rows of eight
-// elements, all its loads whole lines too.  One pass over the parts, four at a time, with
-// a running maximum.
+// threads (a query row each) can store it with whole lines; a warp joins 32 rows of four
+// elements, all its loads whole lines too.  One pass over the parts, eight at a time, with
+// a running maximum (a question of 33 tokens, 18 parts of 165 rows: 44 us in all; eight
+// elements and four parts at a time 46).
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads)
     cache_attn_merge_cols(const CacheAttnArgs a, const AttnShape shape, int64_t items, int ctas,
                           int by_item, const float2* ml,
                           const float4* o) {
-  constexpr int AHEAD = 4;
+  constexpr int AHEAD = 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Split sp = find_split(a, shape, items, ctas, by_item);
   const AttnItem& it = sp.it;
   begin_after_previous();                // the partial results are complete and visible
 
-  const int tasks = sp.parts > 0 ? ((it.rows + 31) / 32) * (D / 8) : 0;
+  const int tasks = sp.parts > 0 ? ((it.rows + 31) / 32) * (D / 4) : 0;
   for (int task = blockIdx.y * kMergeWarps + warp; task < tasks; task += gridDim.y * kMergeWarps) {
-    const int chunk = task % (D / 8), row = task / (D / 8) * 32 + lane;   // elements 8 chunk ..
+    const int chunk = task % (D / 4), row = task / (D / 4) * 32 + lane;   // elements 4 chunk ..
     if (row >= it.rows) continue;
     float M = -INFINITY, L = 0.f;
-    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < sp.parts; i0 += AHEAD) {
       float2 x[AHEAD];
-      float4 p[AHEAD], q[AHEAD];
+      float4 p[AHEAD];
       float top = M;
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
         x[k] = make_float2(-INFINITY, 0.f);
-        p[k] = q[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        p[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i0 + k < sp.parts) {
           const int64_t s = sp.slot(i0 + k);
           x[k] = __ldcg(ml + s * shape.block + row);
-          const float4* part = o + (s * (D / 4) + 2 * chunk) * shape.block + row;
-          p[k] = __ldcg(part);
-          q[k] = __ldcg(part + shape.block);
+          p[k] = __ldcg(o + (s * (D / 4) + chunk) * shape.block + row);
         }
       }
 #pragma unroll
@@ -266,7 +265,6 @@ __global__ void __launch_bounds__(kMergeThreads)
       M = top;
       L *= f;
       u = make_float4(u.x * f, u.y * f, u.z * f, u.w * f);
-      v = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
 #pragma unroll
       for (int k = 0; k < AHEAD; ++k) {
         const float w = exp2f(x[k].x - sub);
@@ -275,17 +273,9 @@ __global__ void __launch_bounds__(kMergeThreads)
         u.y = fmaf(p[k].y, w, u.y);
         u.z = fmaf(p[k].z, w, u.z);
         u.w = fmaf(p[k].w, w, u.w);
-        v.x = fmaf(q[k].x, w, v.x);
-        v.y = fmaf(q[k].y, w, v.y);
-        v.z = fmaf(q[k].z, w, v.z);
-        v.w = fmaf(q[k].w, w, v.w);
       }
     }
-    const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
-    float r[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = L == 0.f ? 0.f : r[i] * inv;
-    attn_store8(a, shape, it, row, 8 * chunk, r);
+    put4(a, shape, it, row, 4 * chunk, u, L);
   }
   put_zeros<D>(a, shape, items);
 }
@@ -296,13 +286,16 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
                               int ctas, bool cols, const float2* ml, const float* o,
                               cudaStream_t st) {
   // y: blocks that share an item's rows.  Few-rows parts: a row a block where an item is
-  // likely to have many parts, else eight; otherwise eight tasks of 32 rows x 8 elements.
+  // likely to have many parts, else eight; otherwise eight tasks of 32 rows x 4 elements.
   const int by_item = items <= ctas;
   const int64_t x = by_item ? items : ctas;
   const int64_t rows = std::min<int64_t>(shape.block, static_cast<int64_t>(shape.n_q) * shape.G);
-  int64_t y = cols ? (rows + 31) / 32 * (a.c.d / 8) / kMergeWarps
+  int64_t y = cols ? (rows + 31) / 32 * (a.c.d / 4) / kMergeWarps
                    : (ctas > kWarpSplits * items ? rows : (rows + kMergeWarps - 1) / kMergeWarps);
-  y = std::max<int64_t>(1, std::min<int64_t>(y, 148 * 8 / x));
+  // (a block finds its item first, which costs as much as joining a few parts: one per cut,
+  // of which most have little to do, comes in fours; 300 us for four questions, 313 in
+  // sixteens)
+  y = std::max<int64_t>(1, std::min<int64_t>(y, 148 * (cols && !by_item ? 4 : 8) / x));
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
   if (cols) {
     const float4* o4 = reinterpret_cast<const float4*>(o);

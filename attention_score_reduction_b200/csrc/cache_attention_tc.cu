@@ -49,12 +49,12 @@
 // what an earlier tile left) are zeroed in V, since 0 * NaN is NaN; in K they give
 // logits that the mask replaces.
 //
-// Measured: 2048 tokens, G = 4, over 8 bf16 heads of 131072 rows together (d = 128):
-// 2.2 ms cold, 2.6 ms under the power cap, 1060 .. 900 TFLOP/s.  A round of two blocks
+// Measured: 2048 tokens, G = 4, over 8 bf16 heads of 573000 rows together (d = 128):
+// 2.2 ms cold, 2.5 ms under the power cap, 1070 .. 950 TFLOP/s.  A round of two blocks
 // is a chain of softmax (1900 cycles), issue and execution of 16 MMAs (1000) and the
 // ways between them (1100), of which the two blocks overlap all but the MMAs.
-// 1024 tokens, G = 2, over 60000 rows: d = 256 bf16 0.59 ms, fp8 1.11 ms, int4 1.03 ms;
-// d = 128 bf16 0.28, fp8 0.52, int4 0.41: unpacking and softmax share the issue slots
+// 1024 tokens, G = 2, over 8 heads of 324000 rows together: d = 256 bf16 0.59 ms, fp8
+// 1.14 ms, int4 1.05 ms; d = 128 bf16 0.28, fp8 0.53, int4 0.42: unpacking and softmax share the issue slots
 // (without the conversions fp8 at d = 256 takes a tenth less, without the per-column
 // powers of two too, without both a quarter less).
 #include <cuda.h>
