@@ -310,19 +310,26 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
                                        by_item, ml, o);
 }
 
-// Up to 16 query rows a unit go to the mma.sync kernel, which reads the cache once
-// for them; beyond, the tensor-memory kernel, whose tiles hold 128.
-static bool few_rows(int n_q, int G) { return static_cast<int64_t>(n_q) * G <= 16; }
+// Few query rows a unit go to the mma.sync kernel, 16 at a time, which each time read the
+// cache again (from L2, mostly); many to the tensor-memory kernel, whose tiles hold 128 and
+// which unpacks quantised pages first.  Measured, rows kernel against the other, us, 284K
+// rows in 8 heads:  bf16 d = 128: 32 rows 42 / 45, 48 75 / 55;  d = 256: 32 108 / 72;
+// fp8 d = 128: 32 35 / 65, 64 57 / 70, 96 82 / 67;  d = 256: 32 66 / 83, 48 102 / 96;
+// int4 d = 128: 64 56 / 65, 96 109 / 86;  d = 256: 32 83 / 95, 48 113 / 89.
+static bool few_rows(int64_t rows, int d, int format) {
+  return rows <= (d == 128 ? 32 : 16) * (format == kFmtBf16 ? 1 : 2);
+}
 
 size_t cache_attn_ws_bytes(int G, int n_q, int d, int format) {
-  if (!few_rows(n_q, G)) return attn_ws_bytes(kTcCtas, tc_block(d), d);
+  if (!few_rows(static_cast<int64_t>(n_q) * G, d, format)) return attn_ws_bytes(kTcCtas, tc_block(d), d);
   const int block = rows_block(static_cast<int64_t>(n_q) * G);
   return attn_ws_bytes(rows_ctas(format, d, block), block, d);
 }
 
 cudaError_t launch_cache_attention(const CacheAttnArgs& a, cudaStream_t s, int* launches) {
-  return few_rows(a.n_q, a.G) ? launch_cache_attn_rows(a, s, launches)
-                              : launch_cache_attn_tc(a, s, launches);
+  return few_rows(static_cast<int64_t>(a.n_q) * a.G, a.c.d, a.c.format)
+             ? launch_cache_attn_rows(a, s, launches)
+             : launch_cache_attn_tc(a, s, launches);
 }
 
 }  // namespace kvzip

@@ -345,7 +345,7 @@ def check_attention(c, q, out, lens, q_lens, scale=None, untouched=None):
     d, G = c.d, q.shape[1]
     scale = 1 / np.sqrt(d) if scale is None else scale
     half = torch.finfo(out.dtype).eps / 2
-    tc = uses_tensor_memory(G, q.shape[2])
+    tc = uses_tensor_memory(c.fmt, d, G, q.shape[2])
     quant = c.fmt != "bf16"
     w = 2.0 ** -11 if quant else (2.0 ** -8 if tc else 2.0 ** -16)
     got = f64(out)
@@ -376,8 +376,8 @@ def check_attention(c, q, out, lens, q_lens, scale=None, untouched=None):
             assert np.all(got[u, :, m:] == untouched)
 
 
-def uses_tensor_memory(G, n_q):
-    return G * n_q > 16
+def uses_tensor_memory(fmt, d, G, n_q):
+    return G * n_q > (32 if d == 128 else 16) * (1 if fmt == "bf16" else 2)
 
 
 def filled(kc, fmt, lens, d, page_rows, seed, capacity=None):
@@ -430,6 +430,21 @@ def test_ragged_chunks(kc, fmt, d, G, n_q):
     for u, n in enumerate(lens):
         blind = max(0, n_q - n)
         assert torch.count_nonzero(out[u, :, :blind]) == 0
+    c.check_status()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d,G,n_q", [(128, 4, 8), (128, 4, 9), (128, 4, 16), (128, 5, 13),
+                                     (128, 64, 1), (256, 4, 4), (256, 4, 8), (256, 3, 11), (256, 32, 1)])
+def test_about_where_the_kernels_change(kc, fmt, d, G, n_q):
+    """Several blocks of 16 query rows a unit, and the first sizes of the other kernel."""
+    lens = [1500, 0, n_q, 3, 77, 130]
+    q_lens = [n_q, 0, n_q, min(3, n_q), max(1, n_q - 3), n_q]
+    c = filled(kc, fmt, lens, d, 32, seed=G + n_q)
+    q = rows_bf16(180 + n_q, len(lens), G, n_q, d).cuda()
+    out = torch.full(q.shape, 7.0, dtype=torch.float32, device="cuda")
+    c.attend(q, q_lens=torch.tensor(q_lens, dtype=torch.int32, device="cuda"), out=out)
+    check_attention(c, q, out, lens, q_lens, untouched=7.0)
     c.check_status()
 
 
