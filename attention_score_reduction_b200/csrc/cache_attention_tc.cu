@@ -50,7 +50,7 @@
 // logits that the mask replaces.
 //
 // Measured: 2048 tokens, G = 4, over 8 bf16 heads of 573000 rows together (d = 128):
-// 2.2 ms cold, 2.5 ms under the power cap, 1070 .. 950 TFLOP/s.  A round of two blocks
+// 2.2 ms cold, 2.6 ms under the power cap, 1070 .. 910 TFLOP/s.  A round of two blocks
 // is a chain of softmax (1900 cycles), issue and execution of 16 MMAs (1000) and the
 // ways between them (1100), of which the two blocks overlap all but the MMAs.
 // 1024 tokens, G = 2, over 8 heads of 324000 rows together: d = 256 bf16 0.59 ms, fp8
