@@ -66,6 +66,7 @@
 
 #include "cache.cuh"
 #include "cache_attention.cuh"
+#include "cache_rings.h"
 #include "cache_sched.cuh"
 #include "kvzip_internal.h"
 #include "sm100_ptx.cuh"
@@ -78,7 +79,8 @@ namespace {
 template <int FMT, int D>
 struct TcaCfg {
   static constexpr bool QUANT = FMT != kFmtBf16;
-  static constexpr int BN = D == 128 ? 128 : 64;       // cache rows of a tile
+  using Rings = TcaRings<QUANT, FMT == kFmtInt4, D>;
+  static constexpr int BN = Rings::BN;                 // cache rows of a tile
   static constexpr int NB = D == 128 ? 2 : 1;          // blocks of 128 query rows
   static constexpr int BLOCK = 128 * NB;               // query rows of an item
   static constexpr int HC = BN / 2;                    // columns of S per softmax thread
@@ -87,8 +89,8 @@ struct TcaCfg {
   static constexpr int KB = D / 64;                    // 128-byte column blocks of a row
   static constexpr int STAGE = BN * D * 2;             // one K or V tile: 32 KB
   static constexpr int Q_BYTES = D == 128 ? NB * 128 * D * 2 : 0;
-  static constexpr int STAGES = QUANT ? 4 : (D == 128 ? 5 : 6);
-  static constexpr int UW = QUANT ? (D == 128 ? 1 : 2) : 0;   // unpacking warpgroups
+  static constexpr int STAGES = Rings::STAGES;
+  static constexpr int UW = Rings::GROUPS;             // unpacking warpgroups
   // warps: loader, two MMA issuers, ends of items (bf16) or row parameters; softmax; unpacking
   static constexpr int SOFT_WARP0 = 4;
   static constexpr int UNPACK_WARP0 = SOFT_WARP0 + 4 * SW;
@@ -96,7 +98,7 @@ struct TcaCfg {
   // quantised pages: pieces of 64 rows as they are stored, codes then parameters
   static constexpr int RB = CacheRow<FMT, D>::BYTES;
   static constexpr int RAW_BYTES = 64 * (RB + 4);
-  static constexpr int RAW_SLOTS = !QUANT ? 0 : (FMT == kFmtFp8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 6));
+  static constexpr int RAW_SLOTS = Rings::RAW_SLOTS;
   // a group of the two has the same stages and slots in every round (a barrier's
   // parity tells two successive phases apart, not three)
   static_assert(UW < 2 || (STAGES % UW == 0 && RAW_SLOTS % UW == 0), "groups share a slot");
@@ -109,14 +111,10 @@ struct TcaCfg {
   static constexpr int OFF_RAW = OFF_KV + STAGES * STAGE;
   // what the unpacking tells the softmax: per V tile e of its pieces (64 rows) or, where
   // a piece's rows differ too much, e of each row, then 2^-e; per K tile the powers of
-  // two of its pieces.  Rings, long enough for how far the
-  // parameters can be ahead of the softmax: the softmax of tile j precedes the
-  // release of V tile j, so at most STAGES + RAW_SLOTS (+ 1) tiles of K and V follow
-  static constexpr int V_RING = 6, K_RING = 8;
+  // two of its pieces.  Rings, as long as the parameters can be ahead of the softmax.
+  static constexpr int V_RING = Rings::V_RING, K_RING = Rings::K_RING;
   static constexpr int OFF_ROWEXP = OFF_RAW + RAW_SLOTS * RAW_BYTES;
   static constexpr int OFF_KSCALE = OFF_ROWEXP + (QUANT ? V_RING * BN * 8 : 0);
-  static_assert(!QUANT || (STAGES + RAW_SLOTS * 64 / BN + 1) / 2 + 1 <= V_RING, "ring of row powers");
-  static_assert(!QUANT || (STAGES + RAW_SLOTS * 64 / BN + 1) / 2 + 2 <= K_RING, "ring of K powers");
   static constexpr int OFF_VSCALE = OFF_KSCALE + (QUANT ? K_RING * 8 : 0);
   static constexpr int OFF_LIFT = OFF_VSCALE + (QUANT ? V_RING * 8 : 0);   // scale of each Q row
   static constexpr int OFF_XCH = OFF_LIFT + (QUANT ? 256 * 4 : 0);       // a float per row
@@ -281,17 +279,9 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
   auto seen_by_all = [&](const AttnItem& it, const Piece& pc) {
     return min(seen_rows(it, it.row0 / shape.G), pc.end);
   };
-  // K and V tiles in the order the MMAs use them: f(is_v, tile).  V tile j comes
-  // after min(j + ahead, n) K tiles and j V tiles.
+  // K and V tiles in the order the MMAs use them: f(is_v, tile).
   auto each_stage = [&](const AttnItem& it, const Piece& pc, auto&& f) -> bool {
-    const int ahead = two_blocks(it) ? 1 : 2;
-    for (int j = 0; j < ahead && j < pc.n; ++j)
-      if (!f(false, j)) return false;
-    for (int j = 0; j < pc.n; ++j) {
-      if (!f(true, j)) return false;
-      if (j + ahead < pc.n && !f(false, j + ahead)) return false;
-    }
-    return true;
+    return for_each_stage(pc.n, two_blocks(it) ? 1 : Cfg::Rings::AHEAD, f);
   };
 
   if (warp < Cfg::SOFT_WARP0) {
