@@ -1,0 +1,128 @@
+"""Attention over the paged cache against its float64 definition, element by element with
+the tolerances of tests/cache_check.py, which tests/test_cache_check.py shows to notice
+wrong results of every kind."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_oracle as co
+from tests import cache_check as cc
+from tests.test_gpu_cache import (FMTS, f64, filled, held_values, make_cache, rows_bf16, slots,
+                                  uses_tensor_memory)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kz():
+    from attention_score_reduction_b200 import build
+    build.build()
+    from attention_score_reduction_b200 import kvzip
+    return kvzip
+
+
+@pytest.fixture(scope="module")
+def kc(kz):
+    from attention_score_reduction_b200 import cache
+    return cache
+
+
+def held(c, side, u, n):
+    """Rows of a unit in float64 on the GPU, in the parts they are stored in."""
+    s = torch.from_numpy(slots(c, u, 0, n)).cuda()
+    pages = getattr(c, side + "_pages")
+    raw = pages.view(-1, pages.shape[2])[s]
+    if c.fmt == "bf16":
+        return cc.Rows(raw.double())
+    par = getattr(c, side + "_params").view(-1)[s].view(-1, 1)
+    if c.fmt == "fp8":
+        table = torch.from_numpy(co.e4m3_value(np.arange(256))).cuda()
+        return cc.Rows(table[raw.long()] * par.view(torch.float32).double())
+    sz = par.view(torch.bfloat16).double()
+    codes = torch.stack((raw & 15, raw >> 4), 2).reshape(n, c.d).double()
+    return cc.Rows(codes * sz[:, :1], sz[:, 1:].expand(n, c.d))
+
+
+def check(c, q, out, lens, q_lens, alike=True, scale=None, units=None):
+    scale = c.d ** -0.5 if scale is None else scale
+    tc = uses_tensor_memory(c.fmt, c.d, q.shape[1], q.shape[2])
+    half = torch.finfo(out.dtype).eps / 2
+    for u in range(len(lens)) if units is None else units:
+        n, m = lens[u], q_lens[u]
+        want, tol = cc.attention(q[u, :, :m].double(), held(c, "k", u, n), held(c, "v", u, n), m, scale,
+                                 c.fmt, tc, half)
+        wrong = cc.close(out[u, :, :m].double(), want, tol, alike)
+        assert wrong is None, (u, n, m, wrong)
+
+
+@pytest.mark.parametrize("G,n_q", [(1, 1), (5, 1), (4, 4), (8, 7), (4, 40), (2, 130), (3, 301)])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_numbers(kc, fmt, d, G, n_q):
+    lens = [n_q + 1900, n_q + 700, n_q, n_q + 64, n_q + 1, n_q + 3333]
+    c = filled(kc, fmt, lens, d, 64, seed=200 + n_q)
+    q = rows_bf16(210 + n_q, len(lens), G, n_q, d).cuda()
+    for dt in (torch.bfloat16, torch.float32):
+        check(c, q, c.attend(q, out_dtype=dt), lens, [n_q] * len(lens))
+    c.check_status()
+
+
+def uneven_values(seed, units, n, d):
+    """V rows whose size changes by powers of two from 64 rows to the next, and by another
+    pattern within them."""
+    v = rows_bf16(seed, units, n, d).float()
+    j = torch.arange(n)
+    e = ((j // 64) * 5 % 13 - 6) * 2 + (j * 7 % 3)
+    return (v * torch.exp2(e.float()).view(1, n, 1)).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("d", [128, 256])
+def test_each_tile_has_its_own_powers(kc, fmt, d):
+    """Items of many tiles beside items of one to five, several to a block, and every output of
+    every call: a tile that took another one's power of two would be far off."""
+    g = torch.Generator().manual_seed(21)
+    lens = torch.randint(400, 5000, (24,), generator=g).tolist()
+    tile = 128 if d == 128 else 64
+    lens += [tile * t - x for t in (1, 2, 3, 4, 5) for x in (0, 1, 13)] * 2
+    order = torch.randperm(len(lens), generator=g).tolist()
+    lens = [lens[i] for i in order]
+    units, n_q, G = len(lens), 200, 3
+    q_lens = [min(n_q - 9 * (u % 5), lens[u]) for u in range(units)]
+    c = make_cache(kc, fmt, [0] * units, d, 128, max(lens), seed=22)
+    k = rows_bf16(220, units, max(lens), d).cuda()
+    v = uneven_values(221, units, max(lens), d).cuda()
+    c.write(k, v, counts=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    q = rows_bf16(222, units, G, n_q, d).cuda()
+    ql = torch.tensor(q_lens, dtype=torch.int32, device="cuda")
+    outs = [torch.zeros_like(q) for _ in range(20)]
+    for o in outs:
+        c.attend(q, q_lens=ql, out=o)
+    torch.cuda.synchronize()
+    check(c, q, outs[0], lens, q_lens, alike=False)
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    c.check_status()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_read_behind_a_fork(kc, fmt):
+    """Rows read on a second stream of a captured graph are the stored rows, rounded once."""
+    c = filled(kc, fmt, [70, 9], 128, 16, seed=23, capacity=90)
+    k, v = rows_bf16(230, 2, 1, 128).cuda(), rows_bf16(231, 2, 1, 128).cuda()
+    back = [torch.zeros(2, 80, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        c.write(k, v)
+        side.wait_stream(main)
+        c.read(n_rows=80, k_out=back[0], v_out=back[1], stream=side)
+        main.wait_stream(side)
+    g.replay()
+    g.replay()
+    assert c.lens.tolist() == [72, 11]
+    for side_name, got in zip("kv", back):
+        for u, n in enumerate((72, 11)):
+            assert np.array_equal(f64(got[u, :n]), co.bf16_round(held_values(c, side_name, u, n)))
+    del g
