@@ -37,9 +37,10 @@
 // kernel bound by issue slots.
 // Q goes to fp16 scaled by a power of two per row (a bf16 value is exact in fp16
 // down to 2^-28 of the row's largest).  The weights p_j s_j are formed relative
-// to a power of two that follows their largest, as fp16: rounded by at most 2^-11
-// of a weight, an eighth of the rounding of a bf16 output.  bf16 caches take the weights as
-// two bf16 parts (about 16 bits).
+// to a power of two that keeps their largest between 2^8 and 2^15, as fp16: rounded by at
+// most 2^-11 of themselves (an eighth of the rounding of a bf16 output) down to 2^-22 of
+// the largest, and by 2^-33 of it below.  bf16 caches take the weights as two bf16 parts
+// (about 16 bits).
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -92,7 +93,21 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
   return v;
 }
 
+// Whether the e4m3 codes of a stored row are zeros, of either sign.
+template <int BYTES>
+__device__ __forceinline__ bool all_zero_codes(uint32_t row) {
+#pragma unroll 1
+  for (int i = 0; i < BYTES; i += 16) {
+    const uint4 v = lds16(row + i);
+    if (((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0) return false;
+  }
+  return true;
+}
+
 constexpr float kCodeUnit = 16777216.f;   // 2^24
+// The largest of the weights that are formed as fp16: held between these, set to 2^11 .. 2^12.
+constexpr float kWeightMax = 32768.f, kWeightMin = 256.f;
+constexpr int kWeightSet = 11;
 constexpr int kRowsTile = 64;     // cache rows of a tile: two or four batches, one per warp
 
 template <int FMT, int D>
@@ -439,6 +454,23 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
           vpar[j] = lds8(slot + 2 * Cfg::CODES + 4 * (BR + 8 * j + 2 * qp));
         }
       }
+      if constexpr (FMT == kFmtFp8) {
+        // a row of zeros is stored with the scale 1, hundreds of times its neighbours': it
+        // must not set the range of the weights
+        constexpr uint32_t kOne = 0x3f800000u;
+        bool one = false;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) one = one || vpar[j].x == kOne || vpar[j].y == kOne;
+        if (__any_sync(0xffffffffu, one)) {
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const uint32_t row = slot + Cfg::CODES + (8 * j + 2 * qp) * RB;
+            if (vpar[j].x == kOne && all_zero_codes<RB>(row)) vpar[j].x = 0u;
+            if (vpar[j].y == kOne && all_zero_codes<RB>(row + RB)) vpar[j].y = 0u;
+          }
+          __syncwarp();
+        }
+      }
       // ---- logits (log2 domain) in place, weights
       uint32_t phi[NT][NJ], plo[NT][QUANT ? 1 : NJ];
       auto softmax = [&](auto mask_tag) {
@@ -512,13 +544,13 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
               ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 2));
               lead[t] = fmaxf(lead[t] * f, ta);
               const float now = lead[t] * F[t];
-              if (lead[t] > 0.f && !(now <= 4096.f && now >= 0.25f)) {
+              if (lead[t] > 0.f && !(now <= kWeightMax && now >= kWeightMin)) {
                 const int e = static_cast<int>(__float_as_uint(lead[t]) >> 23);
-                const float fn = __uint_as_float(static_cast<uint32_t>(min(max(254 - e, 1), 253)) << 23);
+                const float fn = __uint_as_float(static_cast<uint32_t>(min(max(254 + kWeightSet - e, 1), 253)) << 23);
                 f *= fn / F[t];
                 F[t] = fn;
               }
-              top[t] = lead[t] > 0.f ? 4096.f / F[t] : 0.f;
+              top[t] = lead[t] > 0.f ? kWeightMax / F[t] : 0.f;
               moved = true;
             }
 #pragma unroll

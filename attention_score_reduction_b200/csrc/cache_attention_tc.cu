@@ -26,8 +26,12 @@
 // The running maximum is only moved when it grows by more than 2^8 (P then stays
 // below 2^8, its rounding relative): O is rescaled in TMEM for a few tiles of an
 // item instead of all.  P is rounded to bf16 (at most 2^-8 of a weight, errors of
-// both signs; fp16 and 2^-11 for quantised caches); the sum of the weights is taken
-// before the rounding, in fp32.
+// both signs); the sum of the weights is taken before the rounding, in fp32.  For
+// quantised caches P is fp16 and lifted by 2^7, to below 2^15: the largest weight times
+// its row's power of two (below) is at least 2^7, others are rounded by at most 2^-11 of
+// themselves down to 2^-21 of it and by 2^-32 of it below.  Without the lift a row that
+// takes nearly all the weight and adds little (the first of a context) left the others
+// 2^-25 of it: 131072 of them were lost.
 //
 // bf16 pages come by TMA, one box per page and 64 elements, 128-byte swizzle.
 // Quantised pages come as they are, by bulk copies into a ring of 64-row pieces,
@@ -43,8 +47,9 @@
 //       that of the row's largest value, s c + z rounded to 2^-11).  It goes into
 //       the weight: with x' = x + e the products are 2^(x' - m) * row, the running
 //       maximum is x''s, and the sum of weights is sum 2^(x' - m) 2^-e.  At d = 128
-//       64 rows share one e, the largest, where none is 2^8 below it: then it is a
-//       constant of the tile and the softmax has nothing to load per column.
+//       64 rows share one e, the largest, where none is more than 2^4 below it: then it
+//       is a constant of the tile and the softmax has nothing to load per column.  A row
+//       of zeros has the smallest e, so that it counts in the sum of weights and not in m.
 // Rows of the last tile that are not part of the item (other data of the page, or
 // what an earlier tile left) are zeroed in V, since 0 * NaN is NaN; in K they give
 // logits that the mask replaces.
@@ -142,6 +147,9 @@ struct TcaCfg {
   // quantised: one power of two for 64 rows of V where it will do, instead of one a row.
   // d = 128: a seventh faster; d = 256: as fast with either, the plainer one
   static constexpr bool ONE_E = QUANT && D == 128;
+  // (rows so much smaller lose that much of P's range)
+  static constexpr int ONE_E_SPAN = 4;
+  static constexpr float LIFT = QUANT ? 7.f : 0.f;      // log2 of what P is multiplied by
   // of 8 pairs of exponentials, those on the FMA pipe (beside the unpacking, issue slots
   // are scarcer: none there is up to a tenth faster than two)
   static constexpr int POLY = QUANT ? 0 : 2;
@@ -166,6 +174,17 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) {
   return (static_cast<uint64_t>(kDescHi) << 32) | lo;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// Whether the e4m3 codes of a stored row are zeros, of either sign.
+template <int BYTES>
+__device__ __forceinline__ bool all_zero_codes(const uint8_t* row) {
+#pragma unroll 1
+  for (int i = 0; i < BYTES; i += 16) {
+    const uint4 v = *reinterpret_cast<const uint4*>(row + i);
+    if (((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0) return false;
+  }
+  return true;
+}
 
 // Byte offset of 16-byte chunk ch (of 64-element column blocks) of tile row r.
 template <int ROWS>
@@ -555,6 +574,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   reinterpret_cast<uint32_t*>(smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES + 64 * Cfg::RB);
               const int live = pc.end - (pc.r0 + j * BN + h);       // rows of the piece that count
               uint32_t par[2];
+              constexpr int kMinE = -50, kMaxE = 50;
               int e[2], ev[2];           // the row's power of two; the one used for V
               bool nan[2], zero[2];
 #pragma unroll
@@ -562,7 +582,12 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                 par[k] = lane + 32 * k < live ? params[lane + 32 * k] : 0u;
                 if constexpr (FMT == kFmtFp8) {
                   nan[k] = par[k] >= 0x7f800000u;
-                  zero[k] = par[k] == 0;                          // no row, or a page that is not there
+                  // no row, or a page that is not there; a row of zeros is stored with the
+                  // scale 1, hundreds of times its neighbours'
+                  zero[k] = par[k] == 0 ||
+                            (is_v && par[k] == 0x3f800000u &&
+                             all_zero_codes<Cfg::RB>(smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES +
+                                                     (lane + 32 * k) * Cfg::RB));
                   e[k] = nan[k] || zero[k] ? -126 : static_cast<int>(par[k] >> 23) - 127;
                 } else {
                   const float sc = bf16_lo(par[k]), z = bf16_hi(par[k]);
@@ -573,22 +598,22 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                 }
                 // V: within 2^+-50, so that 2^(x' - m) of no row underflows beside another's
                 // that matters no more; fp16 holds what is beyond, up to 2^64
-                ev[k] = nan[k] || zero[k] ? 0 : min(max(e[k], -50), 50);
+                ev[k] = nan[k] ? 0 : (zero[k] ? kMinE : min(max(e[k], kMinE), kMaxE));
               }
-              // V: one power of two for the 64 rows, too, if none is 2^8 below the largest
+              // V: one power of two for the 64 rows, too, if none is far below the largest
               // (their products with it are exact, or as good as their own)
               bool own_e = is_v && !Cfg::ONE_E;
               if (Cfg::ONE_E && is_v) {
                 int hi = -1000, lo = 1000;
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                  if (!zero[k]) {
+                  if (lane + 32 * k < live) {
                     hi = max(hi, ev[k]);
                     lo = min(lo, nan[k] ? -1000 : ev[k]);
                   }
                 hi = __reduce_max_sync(0xffffffffu, hi);
                 lo = __reduce_min_sync(0xffffffffu, lo);
-                own_e = hi - lo > 8;
+                own_e = hi - lo > Cfg::ONE_E_SPAN;
                 if (hi == -1000) hi = 0;
                 if (!own_e) ev[0] = ev[1] = hi;
                 if (lane == 0)
@@ -871,7 +896,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
           l *= f;
           m = cand;
         }
-        float nb = m == -INFINITY ? 0.f : (Cfg::QUANT ? -m : -m * c);
+        float nb = m == -INFINITY ? 0.f : (Cfg::QUANT ? Cfg::LIFT - m : -m * c);
         if (Cfg::QUANT && !own_e) nb += e_all;
         const float2 ce2 = make_float2(ce, ce), nb2 = make_float2(nb, nb);
         float2 acc[4];

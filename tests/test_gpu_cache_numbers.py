@@ -43,7 +43,7 @@ def held(c, side, u, n):
     return cc.Rows(codes * sz[:, :1], sz[:, 1:].expand(n, c.d))
 
 
-def check(c, q, out, lens, q_lens, alike=True, scale=None, units=None):
+def check(c, q, out, lens, q_lens, alike=True, scale=None, units=None, common=0.0):
     scale = c.d ** -0.5 if scale is None else scale
     tc = uses_tensor_memory(c.fmt, c.d, q.shape[1], q.shape[2])
     half = torch.finfo(out.dtype).eps / 2
@@ -51,7 +51,7 @@ def check(c, q, out, lens, q_lens, alike=True, scale=None, units=None):
         n, m = lens[u], q_lens[u]
         want, tol = cc.attention(q[u, :, :m].double(), held(c, "k", u, n), held(c, "v", u, n), m, scale,
                                  c.fmt, tc, half)
-        wrong = cc.close(out[u, :, :m].double(), want, tol, alike)
+        wrong = cc.close(out[u, :, :m].double(), want, tol, alike, common)
         assert wrong is None, (u, n, m, wrong)
 
 
@@ -126,3 +126,41 @@ def test_read_behind_a_fork(kc, fmt):
         for u, n in enumerate((72, 11)):
             assert np.array_equal(f64(got[u, :n]), co.bf16_round(held_values(c, side_name, u, n)))
     del g
+
+
+@pytest.mark.parametrize("gap", [18, 25, 28, 33])
+@pytest.mark.parametrize("sink", ["zero", "small", "alike"])
+@pytest.mark.parametrize("d,n_q", [(128, 1), (128, 40), (256, 1), (256, 40)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_sink_at_the_start_of_a_long_cache(kc, fmt, d, n_q, sink, gap):
+    """One row takes nearly all the weight, 2^gap times another's, and adds little or nothing:
+    the output is then the sum of the others, each far below fp16's normal numbers.  Once with
+    the rows shared out to all blocks, once with so many units on the same pages that a block
+    walks all rows of one."""
+    n, G, m = 70000, 2, n_q
+    one = make_cache(kc, fmt, [0], d, 128, n, seed=24)
+    k, v = rows_bf16(240, 1, n, d), rows_bf16(241, 1, n, d)
+    k[:, :, 0] = 0.0
+    k[0, 0] = 0.0
+    k[0, 0, 0] = gap / (8.0 * d ** -0.5 * 1.4427)
+    if sink != "alike":
+        v[0, 0] = 0.0 if sink == "zero" else v[0, 0] * 2.0 ** -7
+    one.write(k.cuda(), v.cuda())
+    q = rows_bf16(242, 1, G, n_q, d)
+    q[..., 0] = 8.0
+    q = q.cuda()
+    out = one.attend(q, out_dtype=torch.float32)
+    # few rows of 4-bit pages: s c and z are summed apart and nearly cancel here, so that
+    # float32's rounding of either is no longer small beside the output
+    alike = sink != "alike" and (fmt != "int4" or n_q > 1)
+    # many: the sink's key is rounded to fp16 like any other, and its weight is in every sum
+    common = 2.0 ** -11 * gap * np.log(2) if fmt == "int4" else 0.0
+    check(one, q, out, [n], [m], alike=alike, common=common)
+    units = 450
+    c = kc.PagedCache(fmt, one.k_pages, one.v_pages, one.k_params, one.v_params,
+                      one.page_table.repeat(units, 1), one.lens.repeat(units))
+    out = c.attend(q.expand(units, -1, -1, -1), out_dtype=torch.float32)
+    check(c, q.expand(units, -1, -1, -1), out, [n] * units, [m] * units, alike=alike, common=common,
+          units=(0, 1, 211, 449))
+    one.check_status()
+    c.check_status()
