@@ -597,7 +597,9 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   e[k] = nan[k] ? -110 : max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
                 }
                 // V: within 2^+-50, so that 2^(x' - m) of no row underflows beside another's
-                // that matters no more; fp16 holds what is beyond, up to 2^64
+                // that matters no more; fp16 holds some of what is beyond.  A row that it
+                // does not hold is NaN for who sees it, as its infinities would reach others
+                if (is_v && e[k] > kMaxE + (FMT == kFmtFp8 ? 7 : 14)) nan[k] = true;
                 ev[k] = nan[k] ? 0 : (zero[k] ? kMinE : min(max(e[k], kMinE), kMaxE));
               }
               // V: one power of two for the 64 rows, too, if none is far below the largest

@@ -500,7 +500,8 @@ size_t kvzip_cache_attention_workspace_size(const kvzip_cache* cache, int G, int
  * Logits and sums are held in float32.  Quantised caches are attended at their
  * values s c + z or code * 2^e; with many query rows a unit (G n_q above 32, at d = 128
  * above 64) these enter the products as fp16 beside a power of two: rows of K lose what is 2^-38
- * below the largest of their 64, and V wants magnitudes within 2^-64 .. 2^64.
+ * below the largest of their 64, and V wants magnitudes within 2^-64 .. 2^64 (smaller ones
+ * lose digits down to zero; a row with larger ones counts as a row of NaN).
  * Rows of K and V that a token does not see do not touch its result, whatever they
  * hold.  A row it sees that holds infinities or NaN leaves it NaN or infinite in those
  * elements; if not all tokens of the call see the row, in any of its elements.

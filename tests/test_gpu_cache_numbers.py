@@ -164,3 +164,37 @@ def test_a_sink_at_the_start_of_a_long_cache(kc, fmt, d, n_q, sink, gap):
           units=(0, 1, 211, 449))
     one.check_status()
     c.check_status()
+
+
+@pytest.mark.parametrize("power", [60, 66, 67, 68, 70, 74, 90])
+@pytest.mark.parametrize("d,n_q", [(128, 1), (128, 40), (256, 1), (256, 40)])
+@pytest.mark.parametrize("fmt", ["fp8", "int4"])
+def test_values_larger_than_the_products_hold(kc, fmt, d, n_q, power):
+    """A V row of magnitude 2^power and a bit: with few query rows it is what it is, with many
+    a row of NaN beyond 2^64, for the tokens that see it and in no way for the others."""
+    lens, G = [300, 200 + n_q], 3
+    c = make_cache(kc, fmt, [0, 0], d, 64, max(lens), seed=25)
+    k, v = rows_bf16(250, 2, max(lens), d), rows_bf16(251, 2, max(lens), d)
+    v[1] *= 2.0 ** -9
+    at = 200 + n_q // 2                         # a token of the chunk, of unit 1
+    v[1, at] = (v[1, at].float().clamp(-1, 1) * 2.0 ** power).to(torch.bfloat16)
+    v[1, at, 7] = 1.0625 * 2.0 ** power
+    c.write(k.cuda(), v.cuda(), counts=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    q = rows_bf16(252, 2, G, n_q, d).cuda()
+    out = c.attend(q, out_dtype=torch.float32)
+    check(c, q[:1], out[:1], lens[:1], [n_q])
+    many = uses_tensor_memory(fmt, d, G, n_q)
+    if many:
+        first = n_q // 2
+        head = kc.PagedCache(fmt, c.k_pages, c.v_pages, c.k_params, c.v_params, c.page_table[1:],
+                             torch.tensor([at], dtype=torch.int32, device="cuda"))
+        half = torch.finfo(torch.float32).eps / 2
+        want, tol = cc.attention(q[1, :, :first].double(), held(head, "k", 0, at), held(head, "v", 0, at),
+                                 first, d ** -0.5, fmt, True, half)
+        assert cc.close(out[1, :, :first].double(), want, tol) is None
+    if many and power >= 66:
+        assert bool(torch.isnan(out[1, :, n_q // 2:]).all())
+    else:
+        want, tol = cc.attention(q[1].double(), held(c, "k", 1, lens[1]), held(c, "v", 1, lens[1]), n_q,
+                                 d ** -0.5, fmt, many, torch.finfo(torch.float32).eps / 2)
+        assert cc.close(out[1].double(), want, tol, alike=False) is None
