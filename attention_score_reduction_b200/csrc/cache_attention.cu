@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
             bad = min(bad, row);
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
           }
+          __syncwarp();                  // other lanes read what this one has cleared
           bad = __reduce_min_sync(0xffffffffu, bad);
 #pragma unroll
           for (int t = 0; t < NT; ++t)

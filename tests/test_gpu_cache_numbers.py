@@ -198,3 +198,24 @@ def test_values_larger_than_the_products_hold(kc, fmt, d, n_q, power):
         want, tol = cc.attention(q[1].double(), held(c, "k", 1, lens[1]), held(c, "v", 1, lens[1]), n_q,
                                  d ** -0.5, fmt, many, torch.finfo(torch.float32).eps / 2)
         assert cc.close(out[1].double(), want, tol, alike=False) is None
+
+
+def test_cleared_rows_are_cleared_for_every_lane(kc):
+    """Few query rows over bf16 pages: lanes that find a row that is not finite clear it in
+    shared memory, others multiply it.  Every call gives earlier tokens the same finite bits."""
+    for d, G, n_q in ((128, 4, 8), (128, 1, 16), (256, 2, 8)):
+        lens = [n_q + 16 * u for u in range(40)]
+        c = filled(kc, "bf16", lens, d, 16, seed=26)
+        kv = torch.full((40, 1, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+        at = torch.tensor([n - 2 for n in lens], dtype=torch.int32, device="cuda")
+        keep = c.lens.clone()
+        c.write(rows_bf16(260, 40, 1, d).cuda(), kv, starts=at)
+        c.lens.copy_(keep)
+        q = rows_bf16(261, 40, G, n_q, d).cuda()
+        outs = [c.attend(q) for _ in range(50)]
+        m = n_q - 2
+        head = kc.PagedCache("bf16", c.k_pages, c.v_pages, None, None, c.page_table, c.lens - 2)
+        check(head, q[:, :, :m], outs[0][:, :, :m], [n - 2 for n in lens], [m] * 40)
+        for o in outs:
+            assert torch.equal(o[:, :, :m], outs[0][:, :, :m])
+            assert bool(torch.isnan(o[:, :, m:]).all())
