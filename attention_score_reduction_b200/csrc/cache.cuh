@@ -98,6 +98,15 @@ __device__ __forceinline__ bool bf16x8_finite(const uint4& v) {
   return ok;
 }
 
+// none of sixteen e4m3 codes is NaN (all ones but the sign)
+__device__ __forceinline__ bool e4m3x16_finite(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) any |= (w[k] & 0x7f7f7f7fu) + 0x01010101u;
+  return (any & 0x80808080u) == 0;
+}
+
 // two floats as bf16x2 (x in the low half), round to nearest even
 __device__ __forceinline__ uint32_t pack_bf16x2(float x, float y) {
   uint32_t r;

@@ -397,15 +397,17 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
       n_slot = n_slot + 1 == Cfg::SLOTS ? 0 : n_slot + 1;
       copies_wait<Cfg::SLOTS - 1>();
       __syncwarp();
-      if constexpr (!QUANT) {
+      if constexpr (FMT != kFmtInt4) {
         // the chunk's own tokens, which not every query row sees, must not reach those as
-        // 0 * NaN: what is not finite becomes zero, and rows that see it NaN
+        // 0 * NaN: what is not finite becomes zero, and rows that see it NaN.  (fp8 rows
+        // written here have finite codes; those of another writer may not)
         if (lim_all < min(r + BR, r_end)) {
           int bad = INT_MAX;
           for (int i = lane; i < Cfg::CODES / 16; i += 32) {
             const int row = r + i / (RB / 16);
             const uint32_t at = slot + Cfg::CODES + 16 * i;
-            if (row < lim_all || row >= r_end || bf16x8_finite(lds16(at))) continue;
+            if (row < lim_all || row >= r_end) continue;
+            if (FMT == kFmtFp8 ? e4m3x16_finite(lds16(at)) : bf16x8_finite(lds16(at))) continue;
             bad = min(bad, row);
             asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
           }

@@ -186,6 +186,20 @@ __device__ __forceinline__ bool all_zero_codes(const uint8_t* row) {
   return true;
 }
 
+// Whether a stored row has e4m3 codes of NaN; clears the row's pieces that do.
+template <int BYTES>
+__device__ __forceinline__ bool clear_nan_codes(uint8_t* row) {
+  bool found = false;
+#pragma unroll 1
+  for (int i = 0; i < BYTES; i += 16) {
+    uint4* at = reinterpret_cast<uint4*>(row + i);
+    if (e4m3x16_finite(*at)) continue;
+    *at = make_uint4(0, 0, 0, 0);
+    found = true;
+  }
+  return found;
+}
+
 // Byte offset of 16-byte chunk ch (of 64-element column blocks) of tile row r.
 template <int ROWS>
 __device__ __forceinline__ uint32_t tile_off(int r, int ch) {
@@ -566,6 +580,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
       uint32_t g = 0, k_tile = 0, v_tile = 0;
       if (a.test_stall == 0)
         each_item([&](const AttnItem& it, const Piece& pc, bool, int64_t) {
+          const int all_see = seen_by_all(it, pc);
           return each_stage(it, pc, [&](bool is_v, int j) {
             for (int h = 0; h < BN; h += 64, ++g) {
               const int rs = g % Cfg::RAW_SLOTS;
@@ -588,6 +603,12 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                             (is_v && par[k] == 0x3f800000u &&
                              all_zero_codes<Cfg::RB>(smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES +
                                                      (lane + 32 * k) * Cfg::RB));
+                  // NaN codes (of another writer) in a V row that not every token sees: the
+                  // codes become zeros, the row one of NaN
+                  const int row = lane + 32 * k;
+                  if (is_v && row < live && pc.r0 + j * BN + h + row >= all_see &&
+                      clear_nan_codes<Cfg::RB>(smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES + row * Cfg::RB))
+                    nan[k] = true;
                   e[k] = nan[k] || zero[k] ? -126 : static_cast<int>(par[k] >> 23) - 127;
                 } else {
                   const float sc = bf16_lo(par[k]), z = bf16_hi(par[k]);

@@ -219,3 +219,35 @@ def test_cleared_rows_are_cleared_for_every_lane(kc):
         for o in outs:
             assert torch.equal(o[:, :, :m], outs[0][:, :, :m])
             assert bool(torch.isnan(o[:, :, m:]).all())
+
+
+@pytest.mark.parametrize("codes", ["all", "one", "and a NaN scale"])
+@pytest.mark.parametrize("d,G,n_q,bad", [(128, 2, 3, 1), (128, 4, 16, 9), (256, 2, 8, 5), (128, 3, 70, 30), (256, 2, 70, 69),
+                                         (128, 2, 300, 299), (256, 1, 300, 40)])
+def test_nan_codes_of_later_tokens(kc, d, G, n_q, bad, codes):
+    """fp8 pages of another writer may hold e4m3's NaN codes.  Tokens that do not see such a
+    row are as they would be without it, those that do are NaN."""
+    lens = [n_q + 41, n_q, n_q + 700]
+    c = filled(kc, "fp8", lens, d, 32, seed=27)
+    at = [n - n_q + bad for n in lens]
+    for u, pos in enumerate(at):
+        s = int(slots(c, u, pos, 1)[0])
+        for side in "kv":
+            row = getattr(c, side + "_pages").view(-1, d)[s]
+            if codes == "one":
+                row[d - 3 - u] = 0xFF if u & 1 else 0x7F
+            else:
+                row.fill_(0x7F)
+            if codes == "and a NaN scale":
+                getattr(c, side + "_params").view(-1)[s] = 0x7FC00000
+    q = rows_bf16(270, 3, G, n_q, d).cuda()
+    out = c.attend(q)
+    head = kc.PagedCache("fp8", c.k_pages, c.v_pages, c.k_params, c.v_params, c.page_table,
+                         torch.tensor(at, dtype=torch.int32, device="cuda"))
+    many = uses_tensor_memory("fp8", d, G, n_q)
+    for u in range(3):
+        want, tol = cc.attention(q[u, :, :bad].double(), held(head, "k", u, at[u]), held(head, "v", u, at[u]),
+                                 bad, d ** -0.5, "fp8", many, torch.finfo(torch.bfloat16).eps / 2)
+        assert cc.close(out[u, :, :bad].double(), want, tol) is None
+    assert bool(torch.isnan(out[:, :, bad:]).all())
+    c.check_status()
