@@ -175,29 +175,25 @@ __device__ __forceinline__ uint64_t desc(uint32_t lo) {
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// Whether the e4m3 codes of a stored row are zeros, of either sign.
+// The parameter of a stored fp8 row of V whose codes have to be looked at.  A row of zeros is
+// stored with the scale 1, hundreds of times its neighbours': 0 instead.  A row that not every
+// token sees (`clear`) may hold NaN codes of another writer: they become zeros, and NaN instead.
 template <int BYTES>
-__device__ __forceinline__ bool all_zero_codes(const uint8_t* row) {
+__device__ __forceinline__ uint32_t looked_at(uint8_t* codes, uint32_t par, bool clear) {
+  uint32_t any = 0;
+  bool bad = false;
 #pragma unroll 1
   for (int i = 0; i < BYTES; i += 16) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + i);
-    if (((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0) return false;
+    uint4* at = reinterpret_cast<uint4*>(codes + i);
+    const uint4 v = *at;
+    any |= v.x | v.y | v.z | v.w;
+    if (clear && !e4m3x16_finite(v)) {
+      *at = make_uint4(0, 0, 0, 0);
+      bad = true;
+    }
   }
-  return true;
-}
-
-// Whether a stored row has e4m3 codes of NaN; clears the row's pieces that do.
-template <int BYTES>
-__device__ __forceinline__ bool clear_nan_codes(uint8_t* row) {
-  bool found = false;
-#pragma unroll 1
-  for (int i = 0; i < BYTES; i += 16) {
-    uint4* at = reinterpret_cast<uint4*>(row + i);
-    if (e4m3x16_finite(*at)) continue;
-    *at = make_uint4(0, 0, 0, 0);
-    found = true;
-  }
-  return found;
+  if (bad) return 0x7fc00000u;
+  return par == 0x3f800000u && (any & 0x7f7f7f7fu) == 0 ? 0u : par;
 }
 
 // Byte offset of 16-byte chunk ch (of 64-element column blocks) of tile row r.
@@ -592,50 +588,59 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
               constexpr int kMinE = -50, kMaxE = 50;
               int e[2], ev[2];           // the row's power of two; the one used for V
               bool nan[2], zero[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                par[k] = lane + 32 * k < live ? params[lane + 32 * k] : 0u;
-                if constexpr (FMT == kFmtFp8) {
-                  nan[k] = par[k] >= 0x7f800000u;
-                  // no row, or a page that is not there; a row of zeros is stored with the
-                  // scale 1, hundreds of times its neighbours'
-                  zero[k] = par[k] == 0 ||
-                            (is_v && par[k] == 0x3f800000u &&
-                             all_zero_codes<Cfg::RB>(smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES +
-                                                     (lane + 32 * k) * Cfg::RB));
-                  // NaN codes (of another writer) in a V row that not every token sees: the
-                  // codes become zeros, the row one of NaN
-                  const int row = lane + 32 * k;
-                  if (is_v && row < live && pc.r0 + j * BN + h + row >= all_see &&
-                      clear_nan_codes<Cfg::RB>(smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES + row * Cfg::RB))
-                    nan[k] = true;
-                  e[k] = nan[k] || zero[k] ? -126 : static_cast<int>(par[k] >> 23) - 127;
-                } else {
-                  const float sc = bf16_lo(par[k]), z = bf16_hi(par[k]);
-                  const float top = fmax_nan(fabsf(z), fabsf(fmaf(15.f, sc, z)));
-                  nan[k] = !(top < INFINITY);
-                  zero[k] = top == 0.f;
-                  e[k] = nan[k] ? -110 : max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
+              int hi = -1000, lo = 1000;
+              // fp8: the codes of V rows that not every token sees are looked at, and once the
+              // parameters are read those of rows with the scale 1
+              const int rows = min(live, 64), open = all_see - (pc.r0 + j * BN + h);
+              bool look = FMT == kFmtFp8 && is_v && open < rows;
+              while (true) {
+                if (FMT == kFmtFp8 && look) {
+#pragma unroll 1
+                  for (int row = lane; row < rows; row += 32)
+                    params[row] = looked_at<Cfg::RB>(smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES + row * Cfg::RB,
+                                                     params[row], row >= open);
+                  __syncwarp();
                 }
-                // V: within 2^+-50, so that 2^(x' - m) of no row underflows beside another's
-                // that matters no more; fp16 holds some of what is beyond.  A row that it
-                // does not hold is NaN for who sees it, as its infinities would reach others
-                if (is_v && e[k] > kMaxE + (FMT == kFmtFp8 ? 7 : 14)) nan[k] = true;
-                ev[k] = nan[k] ? 0 : (zero[k] ? kMinE : min(max(e[k], kMinE), kMaxE));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  par[k] = lane + 32 * k < live ? params[lane + 32 * k] : 0u;
+                  if constexpr (FMT == kFmtFp8) {
+                    nan[k] = par[k] >= 0x7f800000u;
+                    zero[k] = par[k] == 0;          // no row, or a page that is not there
+                    e[k] = nan[k] || zero[k] ? -126 : static_cast<int>(par[k] >> 23) - 127;
+                  } else {
+                    const float sc = bf16_lo(par[k]), z = bf16_hi(par[k]);
+                    const float top = fmax_nan(fabsf(z), fabsf(fmaf(15.f, sc, z)));
+                    nan[k] = !(top < INFINITY);
+                    zero[k] = top == 0.f;
+                    e[k] = nan[k] ? -110 : max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -110);
+                  }
+                  // V: within 2^+-50, so that 2^(x' - m) of no row underflows beside another's
+                  // that matters no more; fp16 holds some of what is beyond.  A row that it
+                  // does not hold is NaN for who sees it, as its infinities would reach others
+                  if (is_v && e[k] > kMaxE + (FMT == kFmtFp8 ? 7 : 14)) nan[k] = true;
+                  ev[k] = nan[k] ? 0 : (zero[k] ? kMinE : min(max(e[k], kMinE), kMaxE));
+                }
+                if (Cfg::ONE_E && is_v) {
+                  hi = -1000;
+                  lo = 1000;
+#pragma unroll
+                  for (int k = 0; k < 2; ++k)
+                    if (lane + 32 * k < live) {
+                      hi = max(hi, ev[k]);
+                      lo = min(lo, nan[k] ? -1000 : ev[k]);
+                    }
+                  hi = __reduce_max_sync(0xffffffffu, hi);
+                  lo = __reduce_min_sync(0xffffffffu, lo);
+                }
+                if (FMT != kFmtFp8 || !is_v || look) break;
+                look = Cfg::ONE_E ? hi >= 0 : __any_sync(0xffffffffu, par[0] == 0x3f800000u || par[1] == 0x3f800000u);
+                if (!look) break;
               }
               // V: one power of two for the 64 rows, too, if none is far below the largest
               // (their products with it are exact, or as good as their own)
               bool own_e = is_v && !Cfg::ONE_E;
               if (Cfg::ONE_E && is_v) {
-                int hi = -1000, lo = 1000;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  if (lane + 32 * k < live) {
-                    hi = max(hi, ev[k]);
-                    lo = min(lo, nan[k] ? -1000 : ev[k]);
-                  }
-                hi = __reduce_max_sync(0xffffffffu, hi);
-                lo = __reduce_min_sync(0xffffffffu, lo);
                 own_e = hi - lo > Cfg::ONE_E_SPAN;
                 if (hi == -1000) hi = 0;
                 if (!own_e) ev[0] = ev[1] = hi;
