@@ -142,15 +142,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -219,6 +212,11 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
     };
     // batch of rows r .. into a slot; rows past the end and of a bad page become zeros
     auto request = [&](int r, uint32_t slot, const int64_t (&base)[GROUPS]) {
+      // parameters, four rows a copy: a lane of the first BR / 4 takes K's, of the next V's
+      const int par_row = 4 * (lane % (BR / 4));
+      const uint32_t par_dst = slot + 2 * Cfg::CODES + 16 * lane;
+      const uint32_t* par_pool = lane < BR / 4 ? a.c.k_params : a.c.v_params;
+      auto base_of_lane = [&](const int64_t (&b)[GROUPS]) { return par_row < 16 ? b[0] : b[GROUPS - 1]; };
       constexpr int CPR = RB / 16, PER = 32 / CPR > 0 ? 32 / CPR : 1;   // chunks a row, rows a copy
       if (r + BR <= r_end && base[0] >= 0 && base[GROUPS - 1] >= 0) {
         // nothing to leave out: a copy takes 512 consecutive bytes of a group
@@ -235,11 +233,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
           }
         }
         if constexpr (QUANT) {
-          if (lane < BR) {
-            const int64_t at = (BR > 16 && lane >= 16 ? base[GROUPS - 1] : base[0]) + (lane & 15);
-            copy4(slot + 2 * Cfg::CODES + 4 * lane, a.c.k_params + at);
-            copy4(slot + 2 * Cfg::CODES + 4 * (BR + lane), a.c.v_params + at);
-          }
+          if (lane < 2 * (BR / 4)) copy16(par_dst, par_pool + base_of_lane(base) + par_row % 16);
         }
         return;
       }
@@ -254,12 +248,10 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
         copy16(dst + Cfg::CODES, static_cast<const uint8_t*>(a.c.v_pages) + at, bytes);
       }
       if constexpr (QUANT) {
-        if (lane < BR) {
-          const int64_t b = BR > 16 && lane >= 16 ? base[GROUPS - 1] : base[0];
-          const int bytes = b >= 0 && r + lane < r_end ? 4 : 0;
-          const int64_t at = bytes ? b + (lane & 15) : 0;
-          copy4(slot + 2 * Cfg::CODES + 4 * lane, a.c.k_params + at, bytes);
-          copy4(slot + 2 * Cfg::CODES + 4 * (BR + lane), a.c.v_params + at, bytes);
+        if (lane < 2 * (BR / 4)) {
+          const int64_t b = base_of_lane(base);
+          const int bytes = b >= 0 ? 4 * max(0, min(4, r_end - r - par_row)) : 0;
+          copy16(par_dst, par_pool + (bytes ? b + par_row % 16 : 0), bytes);
         }
       }
     };
