@@ -105,6 +105,9 @@ __device__ __forceinline__ bool all_zero_codes(uint32_t row) {
 }
 
 constexpr float kCodeUnit = 16777216.f;   // 2^24
+// How far (log2) a row's running maximum may be above the reference of its weights.  Sums of
+// weights times values stay finite for values up to 2^96 of 2^23 rows.
+constexpr float kLag = 8.f;
 // The largest of the weights that are formed as fp16: held between these, set to 2^11 .. 2^12.
 constexpr float kWeightMax = 32768.f, kWeightMin = 256.f;
 constexpr int kWeightSet = 11;
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
     }
 
     // State of the query rows this lane has in the logits.  Weights are p = 2^(x - m) with
-    // a reference m that follows a row's running maximum only once that is 2^30 above it
+    // a reference m that follows a row's running maximum only once that is 2^8 above it
     // (32-bit sums bear it): no exchange between lanes and no rescaling in most batches.
     // l: this lane's sums of p, by column parity.  Quantised: weights p s are formed as
     // fp16 times a power of two F; F moves when one exceeds top, or (none so far, top = 0)
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
           }
           bool moved = false;
           float f = 1.f;
-          if (__any_sync(0xffffffffu, mx > m[t] + 30.f)) {
+          if (__any_sync(0xffffffffu, mx > m[t] + kLag)) {
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             const float m_new = fmaxf(m[t], mx);

@@ -497,7 +497,8 @@ size_t kvzip_cache_attention_workspace_size(const kvzip_cache* cache, int G, int
  *         m are left as they were.
  *   G     1 .. 64 query heads per unit; scale <= 0 or NaN selects 1/sqrt(d).
  *   q, out 16-byte aligned; workspace 256-byte aligned.
- * Logits and sums are held in float32.  Quantised caches are attended at their
+ * Logits and sums are held in float32; magnitudes of V up to 2^96 stay finite in them.
+ * Quantised caches are attended at their
  * values s c + z or code * 2^e; with many query rows a unit (G n_q above 32, at d = 128
  * above 64) these enter the products as fp16 beside a power of two: rows of K lose what is 2^-38
  * below the largest of their 64, and V wants magnitudes within 2^-64 .. 2^64 (smaller ones

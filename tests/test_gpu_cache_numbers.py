@@ -251,3 +251,25 @@ def test_nan_codes_of_later_tokens(kc, d, G, n_q, bad, codes):
         assert cc.close(out[u, :, :bad].double(), want, tol) is None
     assert bool(torch.isnan(out[:, :, bad:]).all())
     c.check_status()
+
+
+@pytest.mark.parametrize("d,n_q", [(128, 1), (256, 1), (128, 40), (256, 40)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_large_values_and_growing_logits(kc, fmt, d, n_q):
+    """Values up to 2^96 (quantised pages and many rows: 2^62) under logits that grow from one
+    row to the next by 2^29 in all: the sums stay finite wherever the weights' reference is."""
+    n, G, units = 2000, 2, 450
+    one = make_cache(kc, fmt, [0], d, 64, n, seed=28)
+    k, v = rows_bf16(280, 1, n, d), rows_bf16(281, 1, n, d)
+    k[0, :, 0] = (torch.linspace(0, 29, n) / (8.0 * d ** -0.5 * 1.4427)).to(torch.bfloat16)
+    many = uses_tensor_memory(fmt, d, G, n_q)
+    v = (0.5 + 0.5 * v.float().abs().clamp(max=1)) * 2.0 ** (62 if many and fmt != "bf16" else 96)
+    v = v.to(torch.bfloat16)
+    one.write(k.cuda(), v.cuda())
+    c = kc.PagedCache(fmt, one.k_pages, one.v_pages, one.k_params, one.v_params,
+                      one.page_table.repeat(units, 1), one.lens.repeat(units))
+    q = rows_bf16(282, 1, G, n_q, d)
+    q[..., 0] = 8.0
+    q = q.cuda().expand(units, -1, -1, -1)
+    out = c.attend(q, out_dtype=torch.float32)
+    check(c, q, out, [n] * units, [n_q] * units, alike=False, units=(0, 1, 224, 449))
