@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
         v[7] = fmaf(y.w, f, v[7]);
       }
       if (whole) {
-        const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
+        const float inv = attn_inverse(shape, it, row, L);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] *= inv;
         attn_store8(a, shape, it, row, e, v);

@@ -3,11 +3,19 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "cache_sched.cuh"
 
 namespace kvzip {
+
+// What a row's sum is multiplied by: 1 / L.  L = 0 where it sees nothing, which gives zeros,
+// or only logits of -infinity, which have no softmax: NaN.
+__device__ __forceinline__ float attn_inverse(const AttnShape& s, const AttnItem& it, int row, float L) {
+  if (L > 0.f) return 1.f / L;
+  return L == 0.f && seen_rows(it, (it.row0 + row) / s.G) <= 0 ? 0.f : NAN;
+}
 
 // Eight consecutive elements of query row `row` of an item.
 __device__ __forceinline__ void attn_store8(const CacheAttnArgs& a, const AttnShape& s,

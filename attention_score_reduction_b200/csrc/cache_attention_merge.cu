@@ -36,14 +36,13 @@ __device__ __forceinline__ void add_part(RowPart<D>& acc, const float* o, float 
   }
 }
 
-// Elements e .. e + 3 of an output row: x / L (0 where L is 0).
+// Elements e .. e + 3 of an output row: x / L.
 __device__ __forceinline__ void put4(const CacheAttnArgs& a, const AttnShape& s, const AttnItem& it,
                                      int row, int e, float4 x, float L) {
   const int r = it.row0 + row, tok = r / s.G, g = r - tok * s.G;
   const int64_t at = it.u * a.o_unit + g * a.o_head + tok * a.o_row + e;
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN);
-  x = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-               : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  const float inv = attn_inverse(s, it, row, L);
+  x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
   if (a.out_f32)
     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = x;
   else

@@ -1002,6 +1002,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
             l = NAN;
       }
       ++n_item;
+      if (m == -INFINITY && l > 0.f) l = 0.f;      // the polynomial's 2^-125 for 2^-infinity
       const float m2 = Cfg::QUANT || m == -INFINITY ? m : m * c;
       // Q's own block is no longer read; of rows that all groups share, block 1 never was
       float2* mls = reinterpret_cast<float2*>(smem + Cfg::OFF_ML +
@@ -1026,7 +1027,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
       const int share = D / (join ? Cfg::SW : 2);
       const int h0 = (join ? sw : half) * share, h1 = h0 + share;
       const uint32_t oa = lane_base + Cfg::O0 + (join ? 0 : t * D);
-      const float inv = !whole ? 1.f : (L > 0.f ? 1.f / L : (L == 0.f ? 0.f : NAN));
+      const float inv = whole ? attn_inverse(shape, it, row, L) : 1.f;
       f0 *= inv;
       f1 *= inv;
       const bool second = join && pc.n > 1;       // block 1's groups had a tile

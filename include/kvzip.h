@@ -504,8 +504,10 @@ size_t kvzip_cache_attention_workspace_size(const kvzip_cache* cache, int G, int
  * below the largest of their 64, and V wants magnitudes within 2^-64 .. 2^64 (smaller ones
  * lose digits down to zero; a row with larger ones counts as a row of NaN).
  * Rows of K and V that a token does not see do not touch its result, whatever they
- * hold.  A row it sees that holds infinities or NaN leaves it NaN or infinite in those
- * elements; if not all tokens of the call see the row, in any of its elements.
+ * hold.  A V row it sees that holds infinities or NaN leaves it NaN or infinite in those
+ * elements; if not all tokens of the call see the row, in any of its elements.  A logit of
+ * NaN or +infinity makes all of them NaN; one of -infinity weighs nothing, and a token that
+ * sees no other is NaN.
  */
 kvzip_status kvzip_cache_attention(const kvzip_cache* cache, const void* q, int64_t q_unit_stride,
                                    int64_t q_head_stride, int64_t q_row_stride, void* out,

@@ -273,3 +273,29 @@ def test_large_values_and_growing_logits(kc, fmt, d, n_q):
     q = q.cuda().expand(units, -1, -1, -1)
     out = c.attend(q, out_dtype=torch.float32)
     check(c, q, out, [n] * units, [n_q] * units, alike=False, units=(0, 1, 224, 449))
+
+
+@pytest.mark.parametrize("d,G,n_q", [(128, 4, 1), (128, 2, 8), (128, 4, 40), (128, 2, 200), (256, 2, 1), (256, 2, 40)])
+def test_logits_of_minus_infinity(kc, d, G, n_q):
+    """bf16 keys of -infinity: such rows weigh nothing, and a token that sees no others has no
+    softmax (NaN), unlike one that sees no rows at all (zeros)."""
+    lens = [600, n_q + 700, 5000, n_q - 1]
+    c = make_cache(kc, "bf16", [0] * 4, d, 64, max(lens), seed=29)
+    k, v = rows_bf16(290, 4, max(lens), d), rows_bf16(291, 4, max(lens), d)
+    inf = float("inf")
+    k[0, :, 0] = -inf
+    k[2, :, 0] = -inf
+    k[1, :300:2, 0] = -inf
+    k[1, 400:600, 0] = -inf                      # whole tiles of them
+    c.write(k.cuda(), v.cuda(), counts=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    q = rows_bf16(292, 4, G, n_q, d)
+    q[..., 0] = 1.0
+    q = q.cuda()
+    out = c.attend(q, out_dtype=torch.float32)
+    assert bool(torch.isnan(out[0]).all()) and bool(torch.isnan(out[2]).all())
+    some = torch.isfinite(k[1, :lens[1], 0]).cuda()
+    kr, vr = (cc.Rows(held(c, side, 1, lens[1]).a[some]) for side in "kv")
+    many = uses_tensor_memory("bf16", d, G, n_q)
+    want, tol = cc.attention(q[1].double(), kr, vr, n_q, d ** -0.5, "bf16", many, 2.0 ** -24)
+    assert cc.close(out[1].double(), want, tol) is None
+    assert torch.count_nonzero(out[3, :, 0]) == 0
