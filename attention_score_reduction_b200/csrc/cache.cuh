@@ -23,7 +23,7 @@ struct CacheRow {
   static constexpr int BYTES = FMT == kFmtBf16 ? 2 * D : (FMT == kFmtFp8 ? D : D / 2);
 };
 
-// Rows a unit can hold (the host keeps it below 2^31).
+// Rows a unit can hold (the host keeps it below 2^31 - 2^12).
 __device__ __forceinline__ int cache_cap(const CacheArgs& c) { return c.max_pages << c.page_shift; }
 
 // n held to [0, hi]; anything outside sets the status bit.

@@ -473,8 +473,10 @@ static kvzip_status cache_args(const kvzip_cache* c, kvzip::CacheArgs* a) {
   if ((1 << shift) != c->page_rows)
     return c->page_rows > 0 ? KVZIP_ERR_UNSUPPORTED : KVZIP_ERR_INVALID_ARG;
   if (c->units < 0 || c->n_pages <= 0 || c->max_pages <= 0) return KVZIP_ERR_INVALID_ARG;
+  // positions are 32-bit in the kernels, which count up to a few tiles past a unit's end
+  constexpr int kPastEnd = 4096;
   if (c->units > (int64_t{1} << 24) || c->n_pages > (INT32_MAX >> shift) ||
-      c->max_pages > (INT32_MAX >> shift))
+      c->max_pages > ((INT32_MAX - kPastEnd) >> shift))
     return KVZIP_ERR_UNSUPPORTED;
   if (!c->k_pages || !c->v_pages || !c->page_table || !c->lens || !c->status)
     return KVZIP_ERR_INVALID_ARG;

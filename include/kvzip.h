@@ -401,7 +401,7 @@ kvzip_status kvzip_decode_attention(const void* q, const void* k_packed, const v
  *   status              one sticky uint32 the kernels OR into; zero it before
  *                       first use, read and clear it with kvzip_workspace_status.
  *   page_rows           16, 32, 64 or 128.   d  128 or 256.
- *   n_pages * page_rows and max_pages * page_rows are below 2^31.
+ *   n_pages * page_rows is below 2^31, max_pages * page_rows below 2^31 - 2^12.
  *
  * Row formats:
  *   KVZIP_CACHE_BF16  2 d bytes.
