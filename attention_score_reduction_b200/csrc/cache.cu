@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kRowThreads, 4)
         slot = cache_slot(a.c, u, static_cast<int>(pos));
       else
         atomicOr(a.c.status, kStatusBadCache);
+      if (!in_bounds(t >= 0 && t < a.n_rows)) slot = -1;
       ksrc = a.offsets ? (r0 + lane) * a.k_row : u * a.k_unit + t * a.k_row;
       vsrc = a.offsets ? (r0 + lane) * a.v_row : u * a.v_unit + t * a.v_row;
     }
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kRowThreads)
 #pragma unroll
     for (int j = 0; j < UNR; ++j) {
       const uint4 kv = row_values<FMT>(kb[j]), vv = row_values<FMT>(vb[j]);
-      if (sl[j] >= 0) {
+      if (sl[j] >= 0 && in_bounds(r0 + i0 + j * RPW + sub < total)) {
         const int64_t o = (r0 + i0 + j * RPW + sub) * D + lr * 8;
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_out) + o) = kv;
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.v_out) + o) = vv;

@@ -36,6 +36,7 @@ __device__ __forceinline__ int held_to(int64_t n, int hi, uint32_t* status) {
 // Pool row of position pos of unit u (0 <= pos < max_pages * page_rows), or -1
 // (and the status bit) where the page table names no page of the pool.
 __device__ __forceinline__ int64_t cache_slot(const CacheArgs& c, int64_t u, int pos) {
+  if (!in_bounds(u >= 0 && u < c.units && pos >= 0 && pos < cache_cap(c))) return -1;
   const int page = c.page_table[u * c.max_pages + (pos >> c.page_shift)];
   if (page < 0 || page >= c.n_pages) {
     atomicOr(c.status, kStatusBadCache);

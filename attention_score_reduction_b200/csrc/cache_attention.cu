@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] *= inv;
         attn_store8(a, shape, it, row, e, v);
-      } else {
+      } else if (slot_in_bounds(shape, slot, gridDim.x, row)) {
         float4* dst = reinterpret_cast<float4*>(o_out + (slot * RQ + row) * D + e);
         dst[0] = make_float4(v[0], v[1], v[2], v[3]);
         dst[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -739,6 +739,8 @@ cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t st, int* launches) 
 }
 
 }  // namespace
+
+cudaError_t bounds_flag_cache_attention(unsigned int* out) { return take_bounds_flag(out); }
 
 // CTAs of the work line: all resident on the 148 SMs at once.
 int rows_ctas(int format, int d, int block) { return 148 * rows_per_sm(format, d, block); }

@@ -17,11 +17,21 @@ __device__ __forceinline__ float attn_inverse(const AttnShape& s, const AttnItem
   return L == 0.f && seen_rows(it, (it.row0 + row) / s.G) <= 0 ? 0.f : NAN;
 }
 
+// Query head g of token tok of an item has an output row.
+__device__ __forceinline__ bool out_in_bounds(const CacheAttnArgs& a, const AttnItem& it, int tok, int g) {
+  return in_bounds(it.u >= 0 && it.u < a.c.units && tok >= 0 && tok < a.n_q && tok < it.m && g >= 0 && g < a.G);
+}
+// Row `row` of a slot is one of the workspace's: two slots a CTA of `block` rows each.
+__device__ __forceinline__ bool slot_in_bounds(const AttnShape& s, int64_t slot, int ctas, int row) {
+  return in_bounds(slot >= 0 && slot < 2 * static_cast<int64_t>(ctas) && row >= 0 && row < s.block);
+}
+
 // Eight consecutive elements of query row `row` of an item.
 __device__ __forceinline__ void attn_store8(const CacheAttnArgs& a, const AttnShape& s,
                                             const AttnItem& it, int row, int e,
                                             const float (&v)[8]) {
   const int r = it.row0 + row, tok = r / s.G, g = r - tok * s.G;
+  if (!out_in_bounds(a, it, tok, g)) return;
   const int64_t at = it.u * a.o_unit + g * a.o_head + tok * a.o_row + e;
   if (a.out_f32) {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);

@@ -40,6 +40,7 @@ __device__ __forceinline__ void add_part(RowPart<D>& acc, const float* o, float 
 __device__ __forceinline__ void put4(const CacheAttnArgs& a, const AttnShape& s, const AttnItem& it,
                                      int row, int e, float4 x, float L) {
   const int r = it.row0 + row, tok = r / s.G, g = r - tok * s.G;
+  if (!out_in_bounds(a, it, tok, g)) return;
   const int64_t at = it.u * a.o_unit + g * a.o_head + tok * a.o_row + e;
   const float inv = attn_inverse(s, it, row, L);
   x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
@@ -97,6 +98,9 @@ __device__ __forceinline__ Split find_split(const CacheAttnArgs& a, const AttnSh
     r.slot0 = line_slot(t.all, r.c0, n, first);
     r.parts = static_cast<int>(line_cta(t.all, first + r.it.n_tiles - 1, n) - r.c0) + 1;
     if (r.parts < 2) r.parts = 0;
+    if (r.parts > 0 && !(slot_in_bounds(shape, r.slot0, ctas, 0) &&
+                         slot_in_bounds(shape, r.slot(r.parts - 1), ctas, r.it.rows - 1)))
+      r.parts = 0;
   }
   return r;
 }
@@ -308,6 +312,8 @@ cudaError_t launch_attn_merge(const CacheAttnArgs& a, const AttnShape& shape, in
                       : launch_after(cache_attn_merge<256>, grid, kMergeThreads, 0, st, a, shape, items, ctas,
                                        by_item, ml, o);
 }
+
+cudaError_t bounds_flag_cache_attention_merge(unsigned int* out) { return take_bounds_flag(out); }
 
 // Few query rows a unit go to the mma.sync kernel, 16 at a time, which each time read the
 // cache again (from L2, mostly); many to the tensor-memory kernel, whose tiles hold 128 and

@@ -1054,7 +1054,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                                   at(i + 4), at(i + 5), at(i + 6), at(i + 7)};
               attn_store8(a, shape, it, row, h + i, x);
             }
-          } else {
+          } else if (slot_in_bounds(shape, slot, gridDim.x, row)) {
             // by fours of elements, then rows: a warp's stores are whole lines
             float4* dst = reinterpret_cast<float4*>(o_out) + (slot * (D / 4) + h / 4) * Cfg::BLOCK + row;
 #pragma unroll
@@ -1063,7 +1063,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
           }
         }
       }
-      if (!whole && live && half == 0 && (t == 0 || two))
+      if (!whole && live && half == 0 && (t == 0 || two) && slot_in_bounds(shape, slot, gridDim.x, row))
         ml_out[slot * Cfg::BLOCK + row] = make_float2(M, L);
       named_barrier_sync(1, kAll);      // (m, l) and both O are read
       tc_fence_before();
@@ -1207,6 +1207,8 @@ cudaError_t launch_tc_fd(const CacheAttnArgs& a, cudaStream_t st, int* launches)
 }
 
 }  // namespace
+
+cudaError_t bounds_flag_cache_attention_tc(unsigned int* out) { return take_bounds_flag(out); }
 
 int tc_block(int d) { return d == 128 ? 256 : 128; }
 

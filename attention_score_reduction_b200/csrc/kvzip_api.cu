@@ -60,7 +60,9 @@ kvzip_status kvzip_debug_bounds_status(void) {
   unsigned int any = 0;
   cudaError_t (*const files[])(unsigned int*) = {
       kvzip::bounds_flag_score, kvzip::bounds_flag_select, kvzip::bounds_flag_select_fused,
-      kvzip::bounds_flag_compact, kvzip::bounds_flag_decode, kvzip::bounds_flag_cache};
+      kvzip::bounds_flag_compact, kvzip::bounds_flag_decode, kvzip::bounds_flag_cache,
+      kvzip::bounds_flag_cache_attention, kvzip::bounds_flag_cache_attention_tc,
+      kvzip::bounds_flag_cache_attention_merge};
   for (auto take : files) {
     unsigned int f = 0;
     if (take(&f) != cudaSuccess) return KVZIP_ERR_CUDA;

@@ -216,6 +216,9 @@ cudaError_t bounds_flag_select_fused(unsigned int* out);
 cudaError_t bounds_flag_compact(unsigned int* out);
 cudaError_t bounds_flag_decode(unsigned int* out);
 cudaError_t bounds_flag_cache(unsigned int* out);
+cudaError_t bounds_flag_cache_attention(unsigned int* out);
+cudaError_t bounds_flag_cache_attention_tc(unsigned int* out);
+cudaError_t bounds_flag_cache_attention_merge(unsigned int* out);
 
 // Scores are ranked by the bits of |s|: for s >= 0 the bit order is the value
 // order, and -0.0 ranks as 0.0 (its raw bits would rank above every score).
