@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
         v[7] = fmaf(y.w, f, v[7]);
       }
       if (whole) {
-        const float inv = attn_inverse(shape, it, row, L);
+        const float inv = attn_inverse(L, seen_rows(it, (it.row0 + row) / shape.G) <= 0);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] *= inv;
         attn_store8(a, shape, it, row, e, v);

@@ -12,9 +12,8 @@ namespace kvzip {
 
 // What a row's sum is multiplied by: 1 / L.  L = 0 where it sees nothing, which gives zeros,
 // or only logits of -infinity, which have no softmax: NaN.
-__device__ __forceinline__ float attn_inverse(const AttnShape& s, const AttnItem& it, int row, float L) {
-  if (L > 0.f) return 1.f / L;
-  return L == 0.f && seen_rows(it, (it.row0 + row) / s.G) <= 0 ? 0.f : NAN;
+__device__ __forceinline__ float attn_inverse(float L, bool blind) {
+  return L > 0.f ? 1.f / L : (L == 0.f && blind ? 0.f : NAN);
 }
 
 // Query head g of token tok of an item has an output row.

@@ -42,7 +42,7 @@ __device__ __forceinline__ void put4(const CacheAttnArgs& a, const AttnShape& s,
   const int r = it.row0 + row, tok = r / s.G, g = r - tok * s.G;
   if (!out_in_bounds(a, it, tok, g)) return;
   const int64_t at = it.u * a.o_unit + g * a.o_head + tok * a.o_row + e;
-  const float inv = attn_inverse(s, it, row, L);
+  const float inv = attn_inverse(L, seen_rows(it, tok) <= 0);
   x = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
   if (a.out_f32)
     *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = x;

@@ -1002,7 +1002,8 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
             l = NAN;
       }
       ++n_item;
-      if (m == -INFINITY && l > 0.f) l = 0.f;      // the polynomial's 2^-125 for 2^-infinity
+      // the polynomial has 2^-125 for 2^-infinity
+      if (Cfg::POLY > 0 && m == -INFINITY && l > 0.f) l = 0.f;
       const float m2 = Cfg::QUANT || m == -INFINITY ? m : m * c;
       // Q's own block is no longer read; of rows that all groups share, block 1 never was
       float2* mls = reinterpret_cast<float2*>(smem + Cfg::OFF_ML +
@@ -1027,7 +1028,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
       const int share = D / (join ? Cfg::SW : 2);
       const int h0 = (join ? sw : half) * share, h1 = h0 + share;
       const uint32_t oa = lane_base + Cfg::O0 + (join ? 0 : t * D);
-      const float inv = whole ? attn_inverse(shape, it, row, L) : 1.f;
+      const float inv = whole ? attn_inverse(L, lim <= 0) : 1.f;
       f0 *= inv;
       f1 *= inv;
       const bool second = join && pc.n > 1;       // block 1's groups had a tile
