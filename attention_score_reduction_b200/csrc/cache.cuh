@@ -120,13 +120,7 @@ __device__ __forceinline__ uint32_t pack_f16x2(float x, float y) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
   return r;
 }
-// two e4m3 codes (low byte first) as f16x2: exact
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(w)));
-  return r;
-}
-// four e4m3 codes as two f16x2
+// four e4m3 codes (low byte first) as two f16x2: exact
 __device__ __forceinline__ void e4m3x4_f16x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"

@@ -515,7 +515,7 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// Maxima and minima that return NaN if an operand is NaN.
+// Maxima that return NaN if an operand is NaN.
 __device__ __forceinline__ float fmax_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
@@ -524,17 +524,6 @@ __device__ __forceinline__ float fmax_nan(float a, float b) {
 __device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
   float y;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-  return y;
-}
-
-__device__ __forceinline__ float fmin_nan(float a, float b) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
-__device__ __forceinline__ float fmin3_nan(float a, float b, float c) {
-  float y;
-  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
 
