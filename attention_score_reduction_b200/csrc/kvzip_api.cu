@@ -480,8 +480,8 @@ static kvzip_status cache_args(const kvzip_cache* c, kvzip::CacheArgs* a) {
   if (c->units > (int64_t{1} << 24) || c->n_pages > (INT32_MAX >> shift) ||
       c->max_pages > ((INT32_MAX - kPastEnd) >> shift))
     return KVZIP_ERR_UNSUPPORTED;
-  if (!c->k_pages || !c->v_pages || !c->page_table || !c->lens || !c->status)
-    return KVZIP_ERR_INVALID_ARG;
+  if (!c->k_pages || !c->v_pages || !c->status) return KVZIP_ERR_INVALID_ARG;
+  if (c->units > 0 && (!c->page_table || !c->lens)) return KVZIP_ERR_INVALID_ARG;
   if (c->format != KVZIP_CACHE_BF16 && (!c->k_params || !c->v_params)) return KVZIP_ERR_INVALID_ARG;
   if (!aligned(c->k_pages, 16) || !aligned(c->v_pages, 16) || !aligned(c->k_params, 16) ||
       !aligned(c->v_params, 16) || !aligned(c->page_table, 4) || !aligned(c->lens, 4) ||
@@ -521,7 +521,7 @@ kvzip_status kvzip_cache_write(const kvzip_cache* cache, const void* k, const vo
   if (st != KVZIP_OK) return st;
   if (n_rows < 0) return KVZIP_ERR_INVALID_ARG;
   if (!rows_ok(cache->units, n_rows, offsets != nullptr)) return KVZIP_ERR_UNSUPPORTED;
-  if (n_rows > 0 && (!k || !v)) return KVZIP_ERR_INVALID_ARG;
+  if (cache->units > 0 && n_rows > 0 && (!k || !v)) return KVZIP_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(starts, 4) || !aligned(counts, 4) ||
       !aligned(offsets, 8))
     return KVZIP_ERR_INVALID_ARG;

@@ -397,7 +397,8 @@ kvzip_status kvzip_decode_attention(const void* q, const void* k_packed, const v
  *   page_table          [units][max_pages] int32: row pos of unit u lies in page
  *                       page_table[u][pos / page_rows], at pos % page_rows.
  *                       Entries past a unit's last page are not read.
- *   lens                [units] int32: rows each unit holds.
+ *   lens                [units] int32: rows each unit holds.  (Both may be NULL where
+ *                       units is 0.)
  *   status              one sticky uint32 the kernels OR into; zero it before
  *                       first use, read and clear it with kvzip_workspace_status.
  *   page_rows           16, 32, 64 or 128.   d  128 or 256.
@@ -460,7 +461,7 @@ typedef struct {
  * starts is NULL, lens[u] (append); lens[u] = start + rows brought.  starts may be
  * lens itself (an append); otherwise the two must not overlap.  Rows past
  * max_pages * page_rows are dropped and recorded in the status word.
- *   k, v  bf16, 16-byte aligned (NULL only if n_rows is 0).
+ *   k, v  bf16, 16-byte aligned (NULL only if n_rows or the cache's units are 0).
  * One launch, or two for an append of packed rows or of more than 32 per unit.
  */
 kvzip_status kvzip_cache_write(const kvzip_cache* cache, const void* k, const void* v,

@@ -4,6 +4,13 @@ import pytest
 from tests.test_cache_host import _attend, _cache, _read, _write, kz  # noqa: F401
 
 
+def test_a_cache_without_units_takes_rows_without_memory(kz):  # noqa: F811
+    c = _cache(kz, units=0, page_table=None, lens=None)
+    assert _write(kz, c, k=None, v=None) == kz.OK and _read(kz, c, k=None, v=None) == kz.OK
+    assert _attend(kz, c, q=None, out=None) == kz.OK
+    assert _write(kz, _cache(kz), k=None) == kz.ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("page_rows", [16, 32, 64, 128])
 def test_units_end_before_positions_do(kz, page_rows):  # noqa: F811
     """The attention kernels look up to a few tiles past a unit's last row with 32-bit

@@ -299,3 +299,60 @@ def test_logits_of_minus_infinity(kc, d, G, n_q):
     want, tol = cc.attention(q[1].double(), kr, vr, n_q, d ** -0.5, "bf16", many, 2.0 ** -24)
     assert cc.close(out[1].double(), want, tol) is None
     assert torch.count_nonzero(out[3, :, 0]) == 0
+
+
+@pytest.mark.parametrize("d,G,n_q", [(128, 4, 1), (128, 4, 40), (128, 2, 200), (256, 2, 1), (256, 2, 40)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rows_of_bad_pages_attend_as_zeros(kc, kz, fmt, d, G, n_q):
+    """Pages outside the pool at the start, amid and at the end of a unit, the chunk's own among
+    them, beside a unit without."""
+    lens, page = [n_q + 900, n_q + 411], 32
+    c = filled(kc, fmt, lens, d, page, seed=30)
+    q = rows_bf16(300, 2, G, n_q, d).cuda()
+    rows = [held(c, side, 0, lens[0]) for side in "kv"]
+    bad = [0, 1, 7, 12, 13, 14, 15, (lens[0] - 1) // page]
+    c.page_table[0, bad] = torch.tensor([-1, c.n_pages, 2 ** 31 - 1, -7, -1, -1, -1, c.n_pages + 5],
+                                        dtype=torch.int32, device="cuda")
+    out = c.attend(q, out_dtype=torch.float32)
+    for r in rows:
+        for p in bad:
+            r.a[p * page:(p + 1) * page] = 0
+        r.b = r.b.clone()
+        for p in bad:
+            r.b[p * page:(p + 1) * page] = 0
+        r.value, r.parts = r.a + r.b, r.a.abs() + r.b.abs()
+    want, tol = cc.attention(q[0].double(), rows[0], rows[1], n_q, d ** -0.5, fmt,
+                             uses_tensor_memory(fmt, d, G, n_q), 2.0 ** -24)
+    assert cc.close(out[0].double(), want, tol) is None
+    check(c, q, out, lens, [n_q, n_q], units=(1,))
+    with pytest.raises(kz.KvzipError):
+        c.check_status()
+    c.check_status()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_calls_with_nothing_to_do(kc, fmt):
+    c = filled(kc, fmt, [30, 7], 128, 16, seed=31, capacity=64)
+    empty = torch.empty(2, 0, 128, dtype=torch.bfloat16, device="cuda")
+    c.write(empty, empty)
+    c.write(empty[0], empty[0], offsets=torch.zeros(3, dtype=torch.int64, device="cuda"))
+    assert c.lens.tolist() == [30, 7]
+    c.write(empty, empty, starts=torch.tensor([12, 5], dtype=torch.int32, device="cuda"))
+    assert c.lens.tolist() == [12, 5]                 # an empty write at a position ends there
+    k, v = c.read(n_rows=0)
+    assert k.shape == v.shape == (2, 0, 128)
+    assert c.attend(torch.empty(2, 3, 0, 128, dtype=torch.bfloat16, device="cuda")).shape == (2, 3, 0, 128)
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = rows_bf16(310, 2, 3, 20, 128).cuda()
+    out = torch.full_like(q, 5.0)
+    c.attend(q, q_lens=zero, out=out)
+    assert bool((out == 5).all())
+    c.lens.zero_()
+    assert torch.count_nonzero(c.attend(q)) == 0 and torch.count_nonzero(c.attend(q[:, :, :1])) == 0
+    c.check_status()
+    none = kc.PagedCache.allocate(fmt, 0, 128, 4, page_rows=16)
+    rows = torch.empty(0, 5, 128, dtype=torch.bfloat16, device="cuda")
+    none.write(rows, rows)
+    assert none.attend(torch.empty(0, 3, 4, 128, dtype=torch.bfloat16, device="cuda")).shape == (0, 3, 4, 128)
+    assert none.read(n_rows=5)[0].shape == (0, 5, 128)
+    none.check_status()
