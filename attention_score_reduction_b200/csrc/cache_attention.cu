@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(RowsCfg<FMT, D>::THREADS, rows_per_sm(FMT, D, 
               if (lead[t] > 0.f && !(now <= kWeightMax && now >= kWeightMin)) {
                 const int e = static_cast<int>(__float_as_uint(lead[t]) >> 23);
                 const float fn = __uint_as_float(static_cast<uint32_t>(min(max(254 + kWeightSet - e, 1), 253)) << 23);
-                f *= fn / F[t];
+                f = f * fn / F[t];         // in this order: fn / F may be infinite where f is 0
                 F[t] = fn;
               }
               top[t] = lead[t] > 0.f ? kWeightMax / F[t] : 0.f;

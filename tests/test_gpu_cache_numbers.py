@@ -356,3 +356,25 @@ def test_calls_with_nothing_to_do(kc, fmt):
     assert none.attend(torch.empty(0, 3, 4, 128, dtype=torch.bfloat16, device="cuda")).shape == (0, 3, 4, 128)
     assert none.read(n_rows=5)[0].shape == (0, 5, 128)
     none.check_status()
+
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("fmt", ["fp8", "int4"])
+def test_weights_range_moves_all_the_way(kc, fmt, d):
+    """Few rows: values of 2^96 first, which logits 2^250 larger then leave nothing of, and values
+    of 2^-115 with those."""
+    n, G, units = 2000, 2, 450
+    one = make_cache(kc, fmt, [0], d, 64, n, seed=32)
+    k, v = rows_bf16(320, 1, n, d), rows_bf16(321, 1, n, d).float()
+    k[0, :, 0] = 0.0
+    k[0, n // 2:, 0] = 250 / (8.0 * d ** -0.5 * 1.4427)
+    v[0, :n // 2] *= 2.0 ** 94
+    v[0, n // 2:] *= 2.0 ** -115
+    one.write(k.cuda(), v.to(torch.bfloat16).cuda())
+    c = kc.PagedCache(fmt, one.k_pages, one.v_pages, one.k_params, one.v_params,
+                      one.page_table.repeat(units, 1), one.lens.repeat(units))
+    q = rows_bf16(322, 1, G, 1, d)
+    q[..., 0] = 8.0
+    q = q.cuda().expand(units, -1, -1, -1)
+    out = c.attend(q, out_dtype=torch.float32)
+    check(c, q, out, [n] * units, [1] * units, alike=False, units=(0, 1, 224, 449))
