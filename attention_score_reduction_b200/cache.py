@@ -76,7 +76,8 @@ class PagedCache:
 
     def reserve(self, rows):
         """Give every unit pages for at least ``rows`` rows in all: an int, or a
-        host sequence of one number per unit.  Pages a unit has stay its own."""
+        host sequence of one number per unit.  Pages a unit has stay its own.  The
+        table changes on the current stream."""
         if self._free is None:
             raise ValueError("reserve() needs a cache made by PagedCache.allocate")
         rows = [int(rows)] * self.units if isinstance(rows, int) else [int(r) for r in rows]
@@ -152,7 +153,7 @@ class PagedCache:
         """Rows into the cache, at positions ``starts`` (int32 [units]; None:
         after the rows held); lengths move on to the end of what was written.
 
-        Dense: k, v [units][n][d] bf16 (any strides, d contiguous), of which unit
+        Dense: k, v [units][n][d] bf16 (d contiguous, rows on 16-byte boundaries), of which unit
         u brings ``counts[u]`` rows (int32 [units]; None: n).  Packed, with
         ``offsets`` (int64 [units + 1]): k, v [rows][d], unit u's at
         offsets[u]:offsets[u + 1].
@@ -204,8 +205,8 @@ class PagedCache:
     def attend(self, q, q_lens=None, out=None, scale: float = 0.0, out_dtype=torch.bfloat16,
                stream=None):
         """Causal attention of each unit's newest tokens over its rows (their own
-        K and V written before): q [units][G][n_q][d] bf16 (any strides, d
-        contiguous), ``q_lens`` (int32 [units]) of the n_q tokens are a unit's own.
+        K and V written before): q [units][G][n_q][d] bf16 (d contiguous, rows on
+        16-byte boundaries), ``q_lens`` (int32 [units]) of the n_q tokens are a unit's own.
         Returns out [units][G][n_q][d] bf16 or float32; rows past q_lens[u] are
         left as they were (fresh outputs: zeros).
         """

@@ -315,9 +315,11 @@ __device__ __forceinline__ uint4 row_values(const RowBits<FMT>& b) {
 // mode 0: lens left to another launch; 1: starts and lens are different buffers,
 // any thread may write lens; 2: append, a warp's chunk is one whole unit.
 // Rows that are not there load from the first row instead (no branch between loads).
-// Two rows of K and of V per step (fp8: one): at four the 4-bit kernel spills or loses
-// half of its warps.  255K packed rows to 4-bit pages and back as bf16 (two launches,
-// 296 MB): 71 us, 4.2 TB/s; one row a step 77, one group a lane 87.
+// Two rows of K and of V per step (fp8: one).  At the 64 registers that four blocks an SM
+// leave, the 4-bit kernel spills (140 bytes stored, 52 loaded a thread); four rows a step
+// spill more or halve the warps.  255K packed rows to 4-bit pages and back as bf16 (two
+// launches, 296 MB): 71 us, 4.2 TB/s; one row a step 77, one group a lane 87.  The write
+// alone is 43 us at 67% issue active and 39% of DRAM: arithmetic and its latency, not HBM.
 template <int FMT, int D>
 __global__ void __launch_bounds__(kRowThreads, 4)
     cache_write_rows(const CacheWriteArgs a, int64_t total, int chunk, int mode) {

@@ -48,12 +48,13 @@ __device__ __forceinline__ int64_t cache_slot(const CacheArgs& c, int64_t u, int
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// First thing in a kernel launched by launch_after: waits for the kernel before it, then
+// First thing in a kernel launched by launch_after: waits for the kernel before it, whose
+// writes (and, as that one waited, those of all before it) are visible then, and only then
 // lets the next one be launched.  Not the other way round: three kernels of a stream would
-// be on an SM together, and the third could find lines in L1 that the first had loaded and
-// the second has since written.  For the same reason what this file's kernels write (pages,
-// parameters, lengths, partial results, outputs) is read by loads that leave nothing in L1
-// (ld_stream*, __ldcg, asynchronous copies), never by read-only ones.
+// be on an SM together, and the wait of the third says nothing of the first's.  Beside that
+// order, what these kernels write (pages, parameters, lengths, partial results, outputs) is
+// read past L1 (ld_stream*, __ldcg, cp.async.cg, bulk and TMA copies), never by read-only
+// loads; what only the caller writes (page tables, offsets, starts, counts) goes through L1.
 __device__ __forceinline__ void begin_after_previous() {
   cudaGridDependencySynchronize();
   cudaTriggerProgrammaticLaunchCompletion();

@@ -24,8 +24,8 @@
 // Measured, a call in a stream: one token over a bf16 layer of 284K rows in 8 heads
 // (145 MB) 34 us, of which 27 go to the loads (5.4 TB/s; CTAs end between 23 and 31 us,
 // as some SMs get more of HBM than others) and the rest to start, join and merge; one
-// token for each of 16 sequences over 4-bit pages (149 MB) 47 us, bound by issue slots
-// (45% active, 12 warps an SM).
+// token for each of 16 sequences over 4-bit pages (149 MB) 48 us: 46% issue active with
+// three warps a scheduler, whose logits, softmax and output of a batch wait for one another.
 //
 // Quantised formats multiply the codes themselves, as fp16, and fold the rows'
 // parameters into logits and weights:
@@ -33,8 +33,9 @@
 // e4m3 codes are exact in fp16.  4-bit codes are not converted at all: masked out of
 // their word, four bits are the fp16 subnormal c 2^-24 (or 16 c 2^-24), which the
 // tensor core multiplies exactly; the powers of two go into Q and the result.
-// Unpacking to fp16 integers instead (two more instructions a pair) left the
-// kernel bound by issue slots.
+// Unpacking to fp16 integers instead takes two more instructions a pair.  The two sums over
+// 4-bit rows are taken apart and may nearly cancel: their float32 rounding, up to n 2^-26 of
+// either over the n rows that a warp walks, is of sum p s c and sum p z, not of the output.
 // Q goes to fp16 scaled by a power of two per row (a bf16 value is exact in fp16
 // down to 2^-28 of the row's largest).  The weights p_j s_j are formed relative
 // to a power of two that keeps their largest between 2^8 and 2^15, as fp16: rounded by at

@@ -55,13 +55,15 @@
 // logits that the mask replaces.
 //
 // Measured: 2048 tokens, G = 4, over 8 bf16 heads of 573000 rows together (d = 128):
-// 2.2 ms cold, 2.6 ms under the power cap, 1070 .. 910 TFLOP/s.  A round of two blocks
+// 2.2 ms cold, 2.6 to 2.7 ms under the power cap, 1070 .. 890 TFLOP/s.  A round of two blocks
 // is a chain of softmax (1900 cycles), issue and execution of 16 MMAs (1000) and the
 // ways between them (1100), of which the two blocks overlap all but the MMAs.
-// 1024 tokens, G = 2, over 8 heads of 324000 rows together: d = 256 bf16 0.59 ms, fp8
-// 1.14 ms, int4 1.05 ms; d = 128 bf16 0.28, fp8 0.53, int4 0.42: unpacking and softmax share the issue slots
-// (without the conversions fp8 at d = 256 takes a tenth less, without the per-column
-// powers of two too, without both a quarter less).
+// 1024 tokens, G = 2, over 8 heads of 324000 rows together, calls one after another: d = 256
+// bf16 0.76 to 0.85 ms (0.59 cold), fp8 1.20, int4 1.06; d = 128 bf16 0.33, fp8 0.54, int4
+// 0.42.  Each item unpacks its unit's rows again, beside a softmax that wants the same issue
+// slots (without the conversions fp8 at d = 256 takes a tenth less, without the per-column
+// powers of two too, without both a quarter less).  A caller who reads such a cache back to
+// bf16 pages once and attends those is faster: d = 256 fp8 0.97, int4 0.90; d = 128 0.44, 0.38.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -1121,7 +1123,8 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   if (row0 + i * RSTEP >= live) code[i] = make_uint4(0, 0, 0, 0);
               }
               // the piece is in registers; the next copy into the slot is the async proxy's,
-              // which nothing else keeps behind these reads
+              // which nothing else keeps behind these reads (without the fence tiles of fp8,
+              // and of 4 bits at d = 128, now and then hold codes of a later piece)
               fence_proxy_async();
               __syncwarp();
               if (lane == 0) mbar_arrive(&raw_empty[rs]);

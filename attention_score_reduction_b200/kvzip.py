@@ -591,7 +591,8 @@ def cache_attention_workspace_size(cache: CacheStruct, G: int, n_q: int) -> int:
 
 def cache_attention(cache: CacheStruct, q, out, workspace, q_lens=None, scale: float = 0.0,
                     stream=None):
-    """kvzip_cache_attention; q, out [units][G][n_q][d] (any strides, d contiguous)."""
+    """kvzip_cache_attention; q, out [units][G][n_q][d] (d contiguous, other strides
+    multiples of 8)."""
     _, G, n_q, _ = q.shape
     qs, os_ = q.stride(), out.stride()
     s = _lib.kvzip_cache_attention(

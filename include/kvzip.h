@@ -498,12 +498,15 @@ size_t kvzip_cache_attention_workspace_size(const kvzip_cache* cache, int G, int
  *         m are left as they were.
  *   G     1 .. 64 query heads per unit; scale <= 0 or NaN selects 1/sqrt(d).
  *   q, out 16-byte aligned; workspace 256-byte aligned.
- * Logits and sums are held in float32; magnitudes of V up to 2^96 stay finite in them.
- * Quantised caches are attended at their
- * values s c + z or code * 2^e; with many query rows a unit (G n_q above 32, at d = 128
- * above 64) these enter the products as fp16 beside a power of two: rows of K lose what is 2^-38
- * below the largest of their 64, and V wants magnitudes within 2^-64 .. 2^64 (smaller ones
- * lose digits down to zero; a row with larger ones counts as a row of NaN).
+ * Logits and sums are held in float32; magnitudes of V up to 2^96 stay finite in them.  The
+ * weights are rounded for the output product, for float32 outputs too: with few query rows a
+ * unit (G n_q up to 32; d = 256: 16) bf16 caches take them as two bf16 parts (2^-16), with
+ * more as one (2^-8); quantised caches as fp16 (2^-11, and no finer than 2^-28 of the largest
+ * weight times value).  Quantised caches are attended at their values s c + z or code * 2^e.
+ * With many query rows a unit (G n_q above 64; d = 256: 32) these enter the products as fp16
+ * beside a power of two: s c + z is rounded to 2^-11, rows of K lose what is 2^-38 below the
+ * largest of their 64, and V wants magnitudes within 2^-64 .. 2^64 (smaller ones lose digits
+ * down to zero; a row with larger ones counts as a row of NaN).
  * Rows of K and V that a token does not see do not touch its result, whatever they
  * hold.  A V row it sees that holds infinities or NaN leaves it NaN or infinite in those
  * elements; if not all tokens of the call see the row, in any of its elements.  A logit of
