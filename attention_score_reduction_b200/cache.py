@@ -32,7 +32,9 @@ class PagedCache:
     """Pools, page table and lengths of one layer's cache, on one GPU.
 
     The tensors given are used as they are (they may be views of a serving
-    engine's pool) and kept alive; ``status`` is a zeroed int32 word.
+    engine's pool) and kept alive; ``status`` is a zeroed int32 word.  Calls run
+    on the current stream or on ``stream``, which has to wait for whatever made
+    their inputs; those may be dropped right after the call.
     """
 
     def __init__(self, fmt: str, k_pages, v_pages, k_params, v_params, page_table, lens,
@@ -128,6 +130,13 @@ class PagedCache:
         if stream is None and torch.cuda.current_device() == self._index:
             return call(*args, _raw_stream(self._index))
         with self._on(stream) as st:
+            if stream is not None:
+                # the caller may drop what it gave before that stream has used it
+                held = (self.k_pages, self.v_pages, self.k_params, self.v_params, self.page_table,
+                        self.lens, self.status)
+                for t in (*args, *held):
+                    if isinstance(t, torch.Tensor) and t.is_cuda:
+                        t.record_stream(stream)
             return call(*args, st)
 
     def _aux(self, name, t, dtype, n):

@@ -378,3 +378,32 @@ def test_weights_range_moves_all_the_way(kc, fmt, d):
     q = q.cuda().expand(units, -1, -1, -1)
     out = c.attend(q, out_dtype=torch.float32)
     check(c, q, out, [n] * units, [1] * units, alike=False, units=(0, 1, 224, 449))
+
+
+def test_inputs_dropped_before_their_stream_has_used_them(kc):
+    """Rows, queries and the cache itself may be temporaries of a call on another stream: their
+    memory is not handed out again before that stream is done."""
+    k, v = rows_bf16(330, 4, 600, 128).cuda(), rows_bf16(331, 4, 600, 128).cuda()
+    q = rows_bf16(332, 4, 4, 40, 128).cuda()
+    ref = kc.PagedCache.allocate("fp8", 4, 128, 60, page_rows=64)
+    ref.reserve(600)
+    ref.write(k, v)
+    want = ref.attend(q)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        c = kc.PagedCache.allocate("fp8", 4, 128, 60, page_rows=64)
+        c.reserve(600)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)               # the calls wait behind this
+        kt, vt, qt = k.clone(), v.clone(), q.clone()
+        s.wait_stream(torch.cuda.current_stream())
+        c.write(kt, vt, stream=s)
+        out = c.attend(qt, stream=s)
+        shapes = [(t.shape, t.dtype) for t in (kt, vt, qt, c.k_pages, c.v_pages, c.k_params, c.page_table, c.lens)]
+        del kt, vt, qt, c
+        junk = [torch.full(sh, 113, dtype=dt, device="cuda") for sh, dt in shapes for _ in range(3)]
+        s.synchronize()
+        assert torch.equal(out, want)
+        del junk
