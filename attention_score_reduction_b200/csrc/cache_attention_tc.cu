@@ -49,7 +49,7 @@
 //       maximum is x''s, and the sum of weights is sum 2^(x' - m) 2^-e.  At d = 128
 //       64 rows share one e, the largest, where none is more than 2^4 below it: then it
 //       is a constant of the tile and the softmax has nothing to load per column.  A row
-//       of zeros has the smallest e, so that it counts in the sum of weights and not in m.
+//       of zeros has e = -88, so that it counts in the sum of weights and hardly in m.
 // Rows of the last tile that are not part of the item (other data of the page, or
 // what an earlier tile left) are zeroed in V, since 0 * NaN is NaN; in K they give
 // logits that the mask replaces.
@@ -82,6 +82,10 @@
 namespace kvzip {
 
 namespace {
+
+// log2 of how far apart rows of V may be that share a power of two: the smaller lose that
+// much of P's range
+constexpr int kOneESpan = 4;
 
 template <int FMT, int D>
 struct TcaCfg {
@@ -149,8 +153,6 @@ struct TcaCfg {
   // quantised: one power of two for 64 rows of V where it will do, instead of one a row.
   // d = 128: a seventh faster; d = 256: as fast with either, the plainer one
   static constexpr bool ONE_E = QUANT && D == 128;
-  // (rows so much smaller lose that much of P's range)
-  static constexpr int ONE_E_SPAN = 4;
   static constexpr float LIFT = QUANT ? 7.f : 0.f;      // log2 of what P is multiplied by
   // of 8 pairs of exponentials, those on the FMA pipe (beside the unpacking, issue slots
   // are scarcer: none there is up to a tenth faster than two)
@@ -587,7 +589,9 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   reinterpret_cast<uint32_t*>(smem + Cfg::OFF_RAW + rs * Cfg::RAW_BYTES + 64 * Cfg::RB);
               const int live = pc.end - (pc.r0 + j * BN + h);       // rows of the piece that count
               uint32_t par[2];
-              constexpr int kMinE = -50, kMaxE = 50;
+              // a row of zeros (its part of the sum of weights, 2^88 times at most 2^15 of them
+              // each, stays finite for 2^22 rows)
+              constexpr int kMinE = -50, kMaxE = 50, kZeroE = -88;
               int e[2], ev[2];           // the row's power of two; the one used for V
               bool nan[2], zero[2];
               int hi = -1000, lo = 1000;
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
                   // that matters no more; fp16 holds some of what is beyond.  A row that it
                   // does not hold is NaN for who sees it, as its infinities would reach others
                   if (is_v && e[k] > kMaxE + (FMT == kFmtFp8 ? 7 : 14)) nan[k] = true;
-                  ev[k] = nan[k] ? 0 : (zero[k] ? kMinE : min(max(e[k], kMinE), kMaxE));
+                  ev[k] = nan[k] ? 0 : (zero[k] ? kZeroE : min(max(e[k], kMinE), kMaxE));
                 }
                 if (Cfg::ONE_E && is_v) {
                   hi = -1000;
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(TcaCfg<FMT, D>::THREADS, 1)
               // (their products with it are exact, or as good as their own)
               bool own_e = is_v && !Cfg::ONE_E;
               if (Cfg::ONE_E && is_v) {
-                own_e = hi - lo > Cfg::ONE_E_SPAN;
+                own_e = hi - lo > kOneESpan;
                 if (hi == -1000) hi = 0;
                 if (!own_e) ev[0] = ev[1] = hi;
                 if (lane == 0)

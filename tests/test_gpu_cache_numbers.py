@@ -128,8 +128,7 @@ def test_read_behind_a_fork(kc, fmt):
     del g
 
 
-@pytest.mark.parametrize("gap", [18, 25, 28, 33])
-@pytest.mark.parametrize("sink", ["zero", "small", "alike"])
+@pytest.mark.parametrize("sink,gap", [(s, g) for s in ("zero", "small", "alike") for g in (18, 25, 28, 33)] + [("zero", 60), ("zero", 80)])
 @pytest.mark.parametrize("d,n_q", [(128, 1), (128, 40), (256, 1), (256, 40)])
 @pytest.mark.parametrize("fmt", FMTS)
 def test_a_sink_at_the_start_of_a_long_cache(kc, fmt, d, n_q, sink, gap):
